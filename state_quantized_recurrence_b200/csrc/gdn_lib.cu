@@ -11,6 +11,7 @@
 
 #include "gdn_qdq.h"
 #include "gdn_common.cuh"
+#include "gdn_host.cuh"
 #include "gdn_backward.cuh"
 #include "gdn_decode.cuh"
 #include "gdn_prefill_simt.cuh"
@@ -39,6 +40,13 @@ gdn_status err_word(unsigned **out) {
   *out = g_err_ptr[dev];
   return GDN_OK;
 }
+
+}  // namespace
+
+// The same word for the library's other host files.
+gdn_status gdn::error_word(unsigned **out) { return err_word(out); }
+
+namespace {
 
 // Limit of the tensor-core kernels' bounded waits: 2 s, or the value of
 // GDN_WAIT_LIMIT_NS (nanoseconds, read at every launch; 0 gives up at the

@@ -1,0 +1,233 @@
+// Host side of the selective state space scan: argument checks, workspaces
+// and launches.
+#include "gdn_host.cuh"
+#include "gdn_layer.h"
+#include "gdn_scan_simt.cuh"
+
+namespace gdn {
+namespace scan {
+
+struct Call {
+  const void *x, *raw, *B, *C;
+  long long xs, rs, bs, cs;
+  const float *A, *D, *bias, *state_in;
+  const int *cu;
+  int n_seq, T, H, P, G, N;
+};
+
+gdn_status check(const Call &c, gdn_dtype dt, bool token) {
+  if (c.n_seq < 0 || c.T < 0 || c.H <= 0 || c.G <= 0 || c.P <= 0 || c.N <= 0 || c.H % c.G)
+    return GDN_ERR_INVALID_ARG;
+  if (!known_dtype(dt)) return GDN_ERR_UNSUPPORTED;
+  if ((c.P != 64 && c.P != 128) || (c.N != 64 && c.N != 128)) return GDN_ERR_UNSUPPORTED;
+  const long long slots = layer::slot_count(c.n_seq, c.T, kChunk, c.cu != nullptr);
+  if ((double)(token ? c.n_seq : slots) * c.H * (c.P / 64) > 2147483647.0) return GDN_ERR_UNSUPPORTED;
+  const long long rows = c.cu ? c.T : (long long)c.n_seq * c.T;
+  if (c.n_seq == 0) return GDN_OK;
+  if (!c.A || !aligned_to(c.A, 4) || !aligned_to(c.D, 4) || !aligned_to(c.bias, 4) ||
+      !aligned_to(c.state_in, 16) || !aligned_to(c.cu, 4))
+    return GDN_ERR_INVALID_ARG;
+  if (rows == 0) return GDN_OK;
+  const size_t e = elem_bytes(dt);
+  const long long v = 16 / (long long)e;
+  if (!c.x || !c.raw || !c.B || !c.C) return GDN_ERR_INVALID_ARG;
+  if (!aligned_to(c.x, 16) || !aligned_to(c.B, 16) || !aligned_to(c.C, 16) || !aligned_to(c.raw, e))
+    return GDN_ERR_INVALID_ARG;
+  if (rows > 1 && (c.xs < (long long)c.H * c.P || c.bs < (long long)c.G * c.N ||
+                   c.cs < (long long)c.G * c.N || c.rs < c.H || c.xs % v || c.bs % v || c.cs % v))
+    return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+template <typename T>
+In<T> typed(const Call &c) {
+  return In<T>{static_cast<const T *>(c.x), static_cast<const T *>(c.raw),
+               static_cast<const T *>(c.B), static_cast<const T *>(c.C),
+               c.xs, c.rs, c.bs, c.cs, c.A, c.D, c.bias, c.state_in, c.cu,
+               c.n_seq, c.T, c.H, c.P, c.G};
+}
+
+unsigned units(const Call &c) { return (unsigned)(c.n_seq * c.H * (c.P / 64)); }
+
+template <typename T>
+gdn_status prefill(const Call &c, void *y, float *state_out, unsigned *err, cudaStream_t st) {
+  const In<T> in = typed<T>(c);
+  if (c.N == 128)
+    sweep_kernel<T, 128, kForward><<<units(c), 256, 0, st>>>(in, nullptr, nullptr,
+                                                             static_cast<T *>(y), state_out, nullptr, err);
+  else
+    sweep_kernel<T, 64, kForward><<<units(c), 256, 0, st>>>(in, nullptr, nullptr,
+                                                            static_cast<T *>(y), state_out, nullptr, err);
+  return launched();
+}
+
+template <typename T>
+gdn_status decode(const Call &c, float *state, void *y, cudaStream_t st) {
+  const In<T> in = typed<T>(c);
+  if (c.N == 128) decode_kernel<T, 128><<<units(c), 256, 0, st>>>(in, state, static_cast<T *>(y));
+  else decode_kernel<T, 64><<<units(c), 256, 0, st>>>(in, state, static_cast<T *>(y));
+  return launched();
+}
+
+// The gradient's workspace, every part a multiple of 16 bytes.
+struct Workspace {
+  long long slots, rows;
+  size_t states, adjoints, dB, dC, part, bytes;
+};
+Workspace workspace(int n_seq, int T, int H, int P, int N, bool packed) {
+  Workspace w;
+  w.slots = layer::slot_count(n_seq, T, kChunk, packed);
+  w.rows = packed ? T : (long long)n_seq * T;
+  w.states = 0;
+  w.adjoints = w.states + (size_t)w.slots * H * N * P * 4;
+  w.dB = w.adjoints + (size_t)w.slots * H * N * P * 4;
+  w.dC = w.dB + (size_t)w.rows * H * N * 4;
+  w.part = w.dC + (size_t)w.rows * H * N * 4;
+  w.bytes = w.part + (size_t)w.slots * H * 16;
+  return w;
+}
+
+struct Grads {
+  const void *dy;
+  const float *dstate_out;
+  void *dx, *draw;
+  float *dA;
+  void *dB, *dC;
+  float *dD, *dbias, *dstate_in;
+};
+
+template <typename T, int N, int P>
+gdn_status backward_shape(const Call &c, const Grads &g, char *ws, unsigned *err, cudaStream_t st) {
+  const In<T> in = typed<T>(c);
+  const Workspace w = workspace(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr);
+  float *states = reinterpret_cast<float *>(ws + w.states);
+  float *adjoints = reinterpret_cast<float *>(ws + w.adjoints);
+  float *dBh = reinterpret_cast<float *>(ws + w.dB), *dCh = reinterpret_cast<float *>(ws + w.dC);
+  float *part = reinterpret_cast<float *>(ws + w.part);
+  const T *dy = static_cast<const T *>(g.dy);
+  sweep_kernel<T, N, kStates><<<units(c), 256, 0, st>>>(in, nullptr, nullptr, nullptr, nullptr, states, err);
+  sweep_kernel<T, N, kAdjoint><<<units(c), 256, 0, st>>>(in, dy, g.dstate_out, nullptr, g.dstate_in,
+                                                         adjoints, err);
+  auto kern = chunk_grad_kernel<T, N, P>;
+  constexpr size_t smem = ChunkLayout<N, P>::bytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  kern<<<(unsigned)(w.slots * c.H), 256, smem, st>>>(in, dy, states, adjoints,
+                                                     static_cast<T *>(g.dx), static_cast<T *>(g.draw),
+                                                     dBh, dCh, part);
+  const long long total = w.rows * c.G * N;
+  if (total > 0) {
+    const long long want = (total + 255) / 256;
+    head_sum_kernel<T><<<(unsigned)(want < 148 * 16 ? want : 148 * 16), 256, 0, st>>>(
+        dBh, dCh, total, c.H / c.G, N, static_cast<T *>(g.dB), static_cast<T *>(g.dC));
+  }
+  head_param_kernel<<<c.H, 128, 0, st>>>(part, w.slots, c.H, g.dA, g.dD, g.dbias);
+  return launched();
+}
+
+template <typename T>
+gdn_status backward(const Call &c, const Grads &g, char *ws, unsigned *err, cudaStream_t st) {
+  if (c.N == 128)
+    return c.P == 128 ? backward_shape<T, 128, 128>(c, g, ws, err, st)
+                      : backward_shape<T, 128, 64>(c, g, ws, err, st);
+  return c.P == 128 ? backward_shape<T, 64, 128>(c, g, ws, err, st)
+                    : backward_shape<T, 64, 64>(c, g, ws, err, st);
+}
+
+}  // namespace scan
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_scan_prefill_workspace_bytes(int n_seq, int T, int H, int P, int G, int N,
+                                        gdn_dtype dtype, int packed) {
+  return 0;
+}
+
+gdn_status gdn_scan_prefill(const void *x, int64_t x_stride, const void *dt_raw,
+                            int64_t dt_stride, const float *A, const void *B, int64_t b_stride,
+                            const void *C, int64_t c_stride, const float *D,
+                            const float *dt_bias, const float *state_in,
+                            const int32_t *cu_seqlens, int n_seq, int T, int H, int P, int G,
+                            int N, gdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                            void *y, float *state_out, void *cuda_stream) {
+  const scan::Call c{x, dt_raw, B, C, x_stride, dt_stride, b_stride, c_stride, A, D, dt_bias,
+                     state_in, cu_seqlens, n_seq, T, H, P, G, N};
+  gdn_status s = scan::check(c, dtype, false);
+  if (s != GDN_OK || n_seq == 0) return s;
+  if (!state_out || !aligned_to(state_out, 16) || (T > 0 && (!y || !aligned_to(y, 16))))
+    return GDN_ERR_INVALID_ARG;
+  const size_t need = gdn_scan_prefill_workspace_bytes(n_seq, T, H, P, G, N, dtype, cu_seqlens != nullptr);
+  if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need))
+    return GDN_ERR_INVALID_ARG;
+  unsigned *err = nullptr;
+  if (cu_seqlens && (s = error_word(&err)) != GDN_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  return dtype == GDN_DTYPE_F32 ? scan::prefill<float>(c, y, state_out, err, st)
+                                : scan::prefill<__nv_bfloat16>(c, y, state_out, err, st);
+}
+
+gdn_status gdn_scan_decode(const void *x, int64_t x_stride, const void *dt_raw,
+                           int64_t dt_stride, const float *A, const void *B, int64_t b_stride,
+                           const void *C, int64_t c_stride, const float *D,
+                           const float *dt_bias, float *state_inout, int n_seq, int H, int P,
+                           int G, int N, gdn_dtype dtype, void *y, void *cuda_stream) {
+  const scan::Call c{x, dt_raw, B, C, x_stride, dt_stride, b_stride, c_stride, A, D, dt_bias,
+                     nullptr, nullptr, n_seq, 1, H, P, G, N};
+  gdn_status s = scan::check(c, dtype, true);
+  if (s != GDN_OK || n_seq == 0) return s;
+  if (!state_inout || !aligned_to(state_inout, 16) || !y || !aligned_to(y, 16))
+    return GDN_ERR_INVALID_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  return dtype == GDN_DTYPE_F32 ? scan::decode<float>(c, state_inout, y, st)
+                                : scan::decode<__nv_bfloat16>(c, state_inout, y, st);
+}
+
+size_t gdn_scan_backward_workspace_bytes(int n_seq, int T, int H, int P, int G, int N,
+                                         gdn_dtype dtype, int packed) {
+  const scan::Call c{nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, nullptr, nullptr, nullptr,
+                     nullptr, nullptr, 0, T, H, P, G, N};
+  if (n_seq <= 0 || scan::check(c, dtype, false) != GDN_OK) return 0;
+  return scan::workspace(n_seq, T, H, P, N, packed != 0).bytes;
+}
+
+gdn_status gdn_scan_backward(const void *x, int64_t x_stride, const void *dt_raw,
+                             int64_t dt_stride, const float *A, const void *B, int64_t b_stride,
+                             const void *C, int64_t c_stride, const float *D,
+                             const float *dt_bias, const float *state_in,
+                             const int32_t *cu_seqlens, int n_seq, int T, int H, int P, int G,
+                             int N, gdn_dtype dtype, const void *dy, const float *dstate_out,
+                             void *workspace, size_t workspace_bytes, void *dx, void *ddt,
+                             float *dA, void *dB, void *dC, float *dD, float *ddt_bias,
+                             float *dstate_in, void *cuda_stream) {
+  const scan::Call c{x, dt_raw, B, C, x_stride, dt_stride, b_stride, c_stride, A, D, dt_bias,
+                     state_in, cu_seqlens, n_seq, T, H, P, G, N};
+  gdn_status s = scan::check(c, dtype, false);
+  if (s != GDN_OK) return s;
+  if (!dA || !dD || !ddt_bias || !aligned_to(dA, 4) || !aligned_to(dD, 4) || !aligned_to(ddt_bias, 4))
+    return GDN_ERR_INVALID_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (n_seq == 0) {
+    for (float *p : {dA, dD, ddt_bias})
+      if (cudaMemsetAsync(p, 0, (size_t)H * 4, st) != cudaSuccess) return GDN_ERR_CUDA;
+    return GDN_OK;
+  }
+  const size_t e = elem_bytes(dtype);
+  if (!dstate_in || !aligned_to(dstate_in, 16) || !aligned_to(dstate_out, 16))
+    return GDN_ERR_INVALID_ARG;
+  if (T > 0 && (!dy || !dx || !ddt || !dB || !dC || !aligned_to(dy, 16) || !aligned_to(dx, 16) ||
+                !aligned_to(ddt, e) || !aligned_to(dB, 16) || !aligned_to(dC, 16)))
+    return GDN_ERR_INVALID_ARG;
+  const size_t need = gdn_scan_backward_workspace_bytes(n_seq, T, H, P, G, N, dtype, cu_seqlens != nullptr);
+  if (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need) return GDN_ERR_INVALID_ARG;
+  unsigned *err = nullptr;
+  if (cu_seqlens && (s = error_word(&err)) != GDN_OK) return s;
+  const scan::Grads g{dy, dstate_out, dx, ddt, dA, dB, dC, dD, ddt_bias, dstate_in};
+  char *ws = static_cast<char *>(workspace);
+  return dtype == GDN_DTYPE_F32 ? scan::backward<float>(c, g, ws, err, st)
+                                : scan::backward<__nv_bfloat16>(c, g, ws, err, st);
+}
+
+}  // extern "C"
