@@ -5,7 +5,8 @@
  * status codes as gdn_qdq.h: every pointer is caller-owned device memory,
  * nothing is allocated, argument errors are returned before any launch, calls
  * are asynchronous on `cuda_stream`, a malformed cu_seqlens skips the
- * sequences concerned (their outputs are left as they were) and is reported by
+ * sequences concerned (their outputs are left as they were; what the other
+ * sequences of that call receive is not defined) and is reported by
  * gdn_last_error().  All sums, states and statistics are fp32; a result is
  * rounded once, to its own type.  Results do not depend on timing: nothing is
  * added in an order that changes from run to run.

@@ -2,6 +2,7 @@
 // and launches.
 #include "gdn_host.cuh"
 #include "gdn_layer.h"
+#include "gdn_scan_mma.cuh"
 #include "gdn_scan_simt.cuh"
 
 namespace gdn {
@@ -21,6 +22,7 @@ gdn_status check(const Call &c, gdn_dtype dt, bool token) {
   if (!known_dtype(dt)) return GDN_ERR_UNSUPPORTED;
   if ((c.P != 64 && c.P != 128) || (c.N != 64 && c.N != 128)) return GDN_ERR_UNSUPPORTED;
   const long long slots = layer::slot_count(c.n_seq, c.T, kChunk, c.cu != nullptr);
+  if (c.T > 0x7fffff00) return GDN_ERR_UNSUPPORTED;  // tiles are counted in 32-bit tokens
   if ((double)(token ? c.n_seq : slots) * c.H * (c.P / 64) > 2147483647.0) return GDN_ERR_UNSUPPORTED;
   const long long rows = c.cu ? c.T : (long long)c.n_seq * c.T;
   if (c.n_seq == 0) return GDN_OK;
@@ -49,15 +51,87 @@ In<T> typed(const Call &c) {
 
 unsigned units(const Call &c) { return (unsigned)(c.n_seq * c.H * (c.P / 64)); }
 
-template <typename T>
-gdn_status prefill(const Call &c, void *y, float *state_out, unsigned *err, cudaStream_t st) {
-  const In<T> in = typed<T>(c);
+// Sequences are cut into runs of chunks where (sequence, head, 64 columns)
+// units alone would leave SMs idle: a first launch forms what each run adds
+// to a zero state, and each run of the second starts from those before it.
+// The first launch costs half of the second's time a chunk; three CTAs are
+// resident on an SM.
+struct Plan {
+  int seg_chunks;   // chunks of a run
+  bool split;
+  long long slots;  // run slots of the call
+  size_t state, decay, copy, bytes;  // workspace parts
+};
+constexpr int kResident = 3 * 148;
+Plan plan(int n_seq, int T, int H, int P, int N, bool packed) {
+  Plan p = {};
+  const long long units = (long long)n_seq * H * (P / 64);
+  const long long chunks = (T + 63LL) / 64;
+  const long long mean = packed && n_seq > 0 ? (chunks + n_seq - 1) / n_seq : chunks;
+  long long seg = chunks > 0 ? chunks : 1;
+  if (units > 0 && units * 3 < kResident * 2LL && mean > 4) {
+    const long long want = (kResident + units - 1) / units;
+    long long s = (mean + want - 1) / want;
+    if (s < 4) s = 4;
+    if (s < seg) {
+      seg = s;
+      p.split = true;
+    }
+  }
+  p.seg_chunks = (int)seg;
+  p.slots = layer::slot_count(n_seq, T, (int)(seg * 64), packed);
+  if (p.split) {
+    p.decay = (size_t)p.slots * H * N * P * 4;
+    p.copy = p.decay + ((size_t)p.slots * H * 4 + 15) / 16 * 16;
+    p.bytes = p.copy + (size_t)n_seq * H * N * P * 4;
+  }
+  return p;
+}
+
+template <int N, int LEAVE, bool REV>
+gdn_status sweep(const In<__nv_bfloat16> &in, const Plan &p, const __nv_bfloat16 *dy,
+                 const float *first, Ends ends, __nv_bfloat16 *y, float *out_state,
+                 uint32_t *chunk_states, unsigned *err, cudaStream_t st) {
+  auto kern = sweep_mma_kernel<N, LEAVE, REV>;
+  constexpr int smem = (int)SweepSmem<N>::bytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  kern<<<(unsigned)(p.slots * in.H * (in.P / 64)), 128, smem, st>>>(in, dy, first, p.seg_chunks, ends, y,
+                                                                    out_state, chunk_states, err);
+  return launched();
+}
+
+template <int N>
+gdn_status prefill_mma(const Call &c, char *ws, void *y, float *state_out, unsigned *err, cudaStream_t st) {
+  In<__nv_bfloat16> in = typed<__nv_bfloat16>(c);
+  const Plan p = plan(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr);
+  Ends ends{reinterpret_cast<float *>(ws + p.state), reinterpret_cast<float *>(ws + p.decay)};
+  if (p.split) {
+    if (in.state_in && in.state_in == state_out) {  // a late run would write what an early one reads
+      float *copy = reinterpret_cast<float *>(ws + p.copy);
+      if (cudaMemcpyAsync(copy, in.state_in, (size_t)c.n_seq * c.H * c.N * c.P * 4,
+                          cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+        return GDN_ERR_CUDA;
+      in.state_in = copy;
+    }
+    const gdn_status s = sweep<N, kEnds, false>(in, p, nullptr, nullptr, ends, nullptr, nullptr, nullptr, err, st);
+    if (s != GDN_OK) return s;
+  }
+  return sweep<N, kY, false>(in, p, nullptr, in.state_in, ends, static_cast<__nv_bfloat16 *>(y), state_out,
+                             nullptr, err, st);
+}
+
+gdn_status prefill(const Call &c, gdn_dtype dt, char *ws, void *y, float *state_out, unsigned *err,
+                   cudaStream_t st) {
+  if (dt == GDN_DTYPE_BF16)
+    return c.N == 128 ? prefill_mma<128>(c, ws, y, state_out, err, st)
+                      : prefill_mma<64>(c, ws, y, state_out, err, st);
+  const In<float> in = typed<float>(c);
+  float *yo = static_cast<float *>(y);
   if (c.N == 128)
-    sweep_kernel<T, 128, kForward><<<units(c), 256, 0, st>>>(in, nullptr, nullptr,
-                                                             static_cast<T *>(y), state_out, nullptr, err);
+    sweep_kernel<float, 128, kForward><<<units(c), 256, 0, st>>>(in, nullptr, nullptr, yo, state_out, nullptr, err);
   else
-    sweep_kernel<T, 64, kForward><<<units(c), 256, 0, st>>>(in, nullptr, nullptr,
-                                                            static_cast<T *>(y), state_out, nullptr, err);
+    sweep_kernel<float, 64, kForward><<<units(c), 256, 0, st>>>(in, nullptr, nullptr, yo, state_out, nullptr, err);
   return launched();
 }
 
@@ -143,7 +217,10 @@ extern "C" {
 
 size_t gdn_scan_prefill_workspace_bytes(int n_seq, int T, int H, int P, int G, int N,
                                         gdn_dtype dtype, int packed) {
-  return 0;
+  const scan::Call c{nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, nullptr, nullptr, nullptr,
+                     nullptr, nullptr, 0, T, H, P, G, N};
+  if (n_seq <= 0 || dtype != GDN_DTYPE_BF16 || scan::check(c, dtype, false) != GDN_OK) return 0;
+  return scan::plan(n_seq, T, H, P, N, packed != 0).bytes;
 }
 
 gdn_status gdn_scan_prefill(const void *x, int64_t x_stride, const void *dt_raw,
@@ -165,8 +242,7 @@ gdn_status gdn_scan_prefill(const void *x, int64_t x_stride, const void *dt_raw,
   unsigned *err = nullptr;
   if (cu_seqlens && (s = error_word(&err)) != GDN_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  return dtype == GDN_DTYPE_F32 ? scan::prefill<float>(c, y, state_out, err, st)
-                                : scan::prefill<__nv_bfloat16>(c, y, state_out, err, st);
+  return scan::prefill(c, dtype, static_cast<char *>(workspace), y, state_out, err, st);
 }
 
 gdn_status gdn_scan_decode(const void *x, int64_t x_stride, const void *dt_raw,

@@ -1,0 +1,464 @@
+// Selective state space scan of bf16 inputs on the tensor cores, 64 tokens
+// (a chunk) at a time.  With c_t the inclusive sum of dt A inside the chunk:
+//   M_ij = (C_i . B_j) e^{c_i - c_j} dt_j  (i >= j)
+//   y = M x + e^{c_i} C_i S_0 + D x,   S_n = e^{c_n} S_0 + sum_j B_j (w_j x_j)^T,
+//   w_j = e^{c_n - c_j} dt_j.
+// A CTA of four warps carries the state of one (sequence, head, 64 columns of
+// P) through a run of chunks.  The state stays in registers as the
+// accumulators of S^T (warp w: columns 16 w .. + 15 of P as rows, all N as
+// columns), a layout that is at once the B operand of C S_0, so the state
+// never passes through shared memory.
+//
+// Precision: x, B, C are exact bf16 operands.  fp32 operands are split into
+// bf16 pieces: two for M and S_0 as they enter y (2^-17 relative, far under
+// y's own bf16 rounding), three for w x as it enters the state (2^-25: the
+// state stays an fp32 quantity).  Everything is accumulated in fp32.
+#pragma once
+
+#include "gdn_scan_simt.cuh"
+
+namespace gdn {
+namespace scan {
+
+__device__ __forceinline__ uint32_t smem_at(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+// d[16 x 8] += a[16 x 16] b[16 x 8]
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes from global memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// (a, b) as bf16 pairs: hi + lo (+ lo2), each the rounding of what is left.
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  hi = bf2_set(a, b);
+  float ha, hb;
+  bf2_get(hi, ha, hb);
+  lo = bf2_set(a - ha, b - hb);
+}
+__device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  float p, q;
+  hi = bf2_set(a, b);
+  bf2_get(hi, p, q);
+  a -= p;
+  b -= q;
+  mid = bf2_set(a, b);
+  bf2_get(mid, p, q);
+  lo = bf2_set(a - p, b - q);
+}
+
+// Address of 16-byte column `ch` of row r in a tile with rows of COLS bf16:
+// the low three bits of the column are exchanged with the row's, so that
+// eight rows of one column lie in different banks.
+template <int COLS>
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int ch) {
+  return tile + (uint32_t)r * (COLS * 2) + ((uint32_t)(ch ^ (r & 7)) << 4);
+}
+// The four 8 x 8 blocks of a 16 x 16 block at (r0, column ch0), rows first
+// (an A operand as it lies, or with .trans a transposed one's columns) ...
+template <int COLS>
+__device__ __forceinline__ uint32_t block_rows(uint32_t tile, int r0, int ch0, int lane) {
+  return tile_at<COLS>(tile, r0 + (lane & 15), ch0 + (lane >> 4));
+}
+// ... and columns first (two B operands of 8 columns as they lie).
+template <int COLS>
+__device__ __forceinline__ uint32_t block_cols(uint32_t tile, int r0, int ch0, int lane) {
+  return tile_at<COLS>(tile, r0 + (lane & 7) + ((lane >> 4) << 3), ch0 + ((lane >> 3) & 1));
+}
+
+// n rows (of 64; the others zero) of COLS bf16 into a tile, by THREADS threads.
+template <int COLS, int THREADS>
+__device__ __forceinline__ void fetch_tile(uint32_t tile, const __nv_bfloat16 *src, long long stride,
+                                           int n, int tid) {
+  constexpr int kCh = COLS / 8;
+#pragma unroll
+  for (int i = tid; i < 64 * kCh; i += THREADS) {
+    const int r = i / kCh, c = i % kCh;
+    copy16(tile_at<COLS>(tile, r, c), src + (r < n ? r * stride : 0) + c * 8, r < n);
+  }
+}
+
+// Decays of one chunk.  The sums are formed in 64 bits in units of log 2 and
+// kept as two floats: differences of neighbours stay exact where the sums
+// themselves are large.
+struct alignas(16) Decays {  // two of them lie side by side and are read in pairs
+  float hi[64], lo[64];   // c_t / ln 2
+  float dt[64], sig[64];  // step, and the slope of its softplus
+  float gam[64];          // e^{c_t}
+  float del[64];          // e^{c_n - c_t}
+  float w[64];            // del * dt
+  float all;              // e^{c_n}: the decay of the state over the chunk
+};
+__device__ __forceinline__ float exp2_of(double v) {
+  const float h = (float)v;
+  const float l = (float)(v - (double)h);
+  return exp2_fast(h) * fmaf(l, 0.693147181f, 1.0f);
+}
+// By one warp, two tokens a lane; tokens past n have step 0 and decay 1.
+__device__ __forceinline__ void decays_of(const In<__nv_bfloat16> &in, long long row0, int n, int h,
+                                          float A, float bias, Decays &m) {
+  const int lane = threadIdx.x & 31;
+  double a[2];
+  float dt[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int t = 2 * lane + k;
+    dt[k] = 0.0f;
+    float sg = 0.0f;
+    if (t < n) {
+      const float v = to_f32(in.raw[(row0 + t) * in.rs + h]) + bias;
+      dt[k] = softplus(v);
+      sg = 1.0f / (1.0f + expf(-v));
+    }
+    m.dt[t] = dt[k];
+    m.sig[t] = sg;
+    // a token that forgets everything counts as 2^-1500 = 0: sums stay finite
+    const double e = (double)dt[k] * (double)A * 1.4426950408889634;
+    a[k] = e < -1500.0 ? -1500.0 : e;
+  }
+  const double own = a[0] + a[1];
+  double inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  const double total = __shfl_sync(0xffffffffu, inc, 31);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int t = 2 * lane + k;
+    const double c = k ? inc : inc - a[1];
+    const float hi = (float)c;
+    m.hi[t] = hi;
+    m.lo[t] = (float)(c - (double)hi);
+    m.gam[t] = exp2_of(c);
+    const float d = exp2_of(total - c);
+    m.del[t] = d;
+    m.w[t] = d * dt[k];
+  }
+  if (lane == 0) m.all = exp2_of(total);
+}
+
+// What a sweep leaves behind.
+enum Leave : int {
+  kY = 0,      // y of every token and the last state
+  kEnds = 1,   // the state that the run adds to zero, and its decay
+  kChunks = 2  // the state at every chunk's start (backwards: end), as bf16 pairs
+};
+
+template <int N>
+struct SweepSmem {
+  static constexpr uint32_t C = 0, B = C + 64 * N * 2, X = B + 64 * N * 2, M = X + 64 * 64 * 2;
+  static constexpr uint32_t D = M + 2 * 64 * 64 * 2;
+  static constexpr uint32_t bytes = D + 2 * sizeof(Decays);
+};
+
+struct Ends {           // kEnds writes, the others read
+  float *state;         // [segment slot][H][N][P]
+  float *decay;         // [segment slot][H]
+};
+
+// REV: the adjoint G backwards over the chunks, G_0 = e^{c_n} G_n + sum_i
+// e^{c_i} C_i dy_i^T, with C in B's place, dy in x's and e^{c_i} in w's.
+template <int N, int LEAVE, bool REV>
+__global__ void __launch_bounds__(128, 3)
+sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ dy,
+                 const float *first_state, int seg_chunks, Ends ends, __nv_bfloat16 *__restrict__ y,
+                 float *out_state, uint32_t *__restrict__ chunk_states, unsigned *err) {
+  using S = SweepSmem<N>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sC = smem_at(smem) + S::C, sB = smem_at(smem) + S::B, sX = smem_at(smem) + S::X;
+  const uint32_t sM = smem_at(smem) + S::M;
+  Decays *dec = reinterpret_cast<Decays *>(smem + S::D);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int npt = in.P / 64;
+  const int pt = blockIdx.x % npt, h = blockIdx.x / npt % in.H;
+  const long long slot = blockIdx.x / npt / in.H;
+  const int grp = h / (in.H / in.G);
+  if (in.cu && blockIdx.x == 0) check_seqlens(in.cu, in.n_seq, in.T_, err);
+  const Tile t = find_tile(in.cu, in.n_seq, in.T_, seg_chunks * 64, slot);
+  if (t.seq < 0) return;
+  const long long row_end = t.start + t.len;
+  const int chunks = (int)((t.len + 63) / 64);            // of the sequence
+  const int segs = max(1, (chunks + seg_chunks - 1) / seg_chunks);
+  const int c0 = t.tile * seg_chunks, c1 = min(chunks, c0 + seg_chunks);
+  const bool last_seg = REV ? t.tile == 0 : t.tile == segs - 1;
+  if (LEAVE == kEnds && last_seg) return;                  // nobody follows
+  const float A = in.A[h], bias = in.bias ? in.bias[h] : 0.0f;
+
+  // the state's (p, n) of this thread: rows 16 warp + g (+ 8) of P, columns
+  // 8 i + 2 q (+ 1) of N
+  float st[N / 8][4];
+  const long long p0 = pt * 64 + warp * 16 + g;
+  const long long np = (long long)N * in.P;
+  {
+    const float *src = LEAVE == kEnds || !first_state ? nullptr
+                       : first_state + ((long long)t.seq * in.H + h) * np + p0;
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        st[i][e] = src ? src[(8 * i + 2 * q + (e & 1)) * (long long)in.P + (e >> 1) * 8] : 0.0f;
+  }
+  if (LEAVE != kEnds) {  // what the runs before this one add
+    const int before = REV ? segs - 1 - t.tile : t.tile;
+    for (int k = 0; k < before; ++k) {
+      const long long s = slot + (REV ? before - k : k - before);
+      const float d = ends.decay[s * in.H + h];
+      const float *src = ends.state + (s * in.H + h) * np + p0;
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          st[i][e] = fmaf(d, st[i][e], src[(8 * i + 2 * q + (e & 1)) * (long long)in.P + (e >> 1) * 8]);
+    }
+  }
+
+  const __nv_bfloat16 *Bp = REV ? in.C + grp * N : in.B + grp * N;
+  const long long Bs = REV ? in.cs : in.bs;
+  const __nv_bfloat16 *Xp = (REV ? dy : in.x) + (long long)h * in.P + pt * 64;
+  const long long Xs = REV ? (long long)in.H * in.P : in.xs;
+  auto chunk_at = [&](int k) { return REV ? c1 - 1 - k : c0 + k; };
+  auto row_of = [&](int c) { return t.start + (long long)c * 64; };
+  auto rows_in = [&](int c) { return (int)min(64LL, row_end - row_of(c)); };
+  const int total = c1 - c0;
+  float run_decay = 1.0f;
+
+  if (total > 0) {
+    const int c = chunk_at(0);
+    if (LEAVE == kY) fetch_tile<N, 128>(sC, in.C + grp * N + row_of(c) * in.cs, in.cs, rows_in(c), tid);
+    fetch_tile<N, 128>(sB, Bp + row_of(c) * Bs, Bs, rows_in(c), tid);
+    fetch_tile<64, 128>(sX, Xp + row_of(c) * Xs, Xs, rows_in(c), tid);
+    copy_commit();
+    if (warp == 0) decays_of(in, row_of(c), rows_in(c), h, A, bias, dec[0]);
+  }
+  const float Dh = LEAVE == kY && in.D ? in.D[h] : 0.0f;
+
+#pragma unroll 1
+  for (int k = 0; k < total; ++k) {
+    const int c = chunk_at(k);
+    const Decays &m = dec[k & 1];
+    copy_wait<0>();
+    __syncthreads();
+
+    if (LEAVE == kChunks) {  // rows p of N bf16: hi, then lo
+      const long long slot64 = in.cu ? t.seq + t.start / 64 + c : (long long)t.seq * chunks + c;
+      uint32_t *o = chunk_states + ((slot64 * in.H + h) * 2) * (np / 2);
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t hi, lo;
+          split2(st[i][2 * e], st[i][2 * e + 1], hi, lo);
+          const long long at = ((p0 + 8 * e) * N + 8 * i + 2 * q) / 2;
+          o[at] = hi;
+          o[np / 2 + at] = lo;
+        }
+    }
+
+    float yv[4][2][4];
+    if constexpr (LEAVE == kY) {
+      // S = C B^T, rows 16 warp .. + 15, columns up to the diagonal
+      float s[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < N / 16; ++kk) {
+        uint32_t a[4];
+        ldsm4(block_rows<N>(sC, warp * 16, 2 * kk, lane), a);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j > warp) break;
+          uint32_t b[4];
+          ldsm4(block_cols<N>(sB, 16 * j, 2 * kk, lane), b);
+          mma16816(s[2 * j], a, b[0], b[1]);
+          mma16816(s[2 * j + 1], a, b[2], b[3]);
+        }
+      }
+      // M as bf16 pairs in shared memory
+      const int r0 = warp * 16 + g;
+      const float h0 = m.hi[r0], l0 = m.lo[r0], h1 = m.hi[r0 + 8], l1 = m.lo[r0 + 8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j > 2 * warp + 1) break;
+        const int cc = 8 * j + 2 * q;
+        const float2 hj = *reinterpret_cast<const float2 *>(&m.hi[cc]);
+        const float2 lj = *reinterpret_cast<const float2 *>(&m.lo[cc]);
+        const float2 dj = *reinterpret_cast<const float2 *>(&m.dt[cc]);
+        const float v0 = r0 >= cc ? s[j][0] * exp2_fast((h0 - hj.x) + (l0 - lj.x)) * dj.x : 0.0f;
+        const float v1 = r0 > cc ? s[j][1] * exp2_fast((h0 - hj.y) + (l0 - lj.y)) * dj.y : 0.0f;
+        const float v2 = r0 + 8 >= cc ? s[j][2] * exp2_fast((h1 - hj.x) + (l1 - lj.x)) * dj.x : 0.0f;
+        const float v3 = r0 + 8 > cc ? s[j][3] * exp2_fast((h1 - hj.y) + (l1 - lj.y)) * dj.y : 0.0f;
+        uint32_t hi, lo;
+        const uint32_t at0 = tile_at<64>(sM, r0, j) + q * 4, at1 = tile_at<64>(sM, r0 + 8, j) + q * 4;
+        split2(v0, v1, hi, lo);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0), "r"(hi) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0 + 8192), "r"(lo) : "memory");
+        split2(v2, v3, hi, lo);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at1), "r"(hi) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at1 + 8192), "r"(lo) : "memory");
+      }
+      // C S_0, the state's pieces straight from the accumulators
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) yv[i][j][e] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < N / 16; ++kk) {
+        uint32_t hb[2][2], lb[2][2];  // [8 columns of P][k half]
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            split2(st[2 * kk + u][2 * e], st[2 * kk + u][2 * e + 1], hb[e][u], lb[e][u]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a[4];
+          ldsm4(block_rows<N>(sC, 16 * i, 2 * kk, lane), a);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mma16816(yv[i][e], a, hb[e][0], hb[e][1]);
+            mma16816(yv[i][e], a, lb[e][0], lb[e][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ga = m.gam[16 * i + g], gb = m.gam[16 * i + g + 8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          yv[i][j][0] *= ga;
+          yv[i][j][1] *= ga;
+          yv[i][j][2] *= gb;
+          yv[i][j][3] *= gb;
+        }
+      }
+      __syncthreads();  // M is there, C is free
+      if (k + 1 < total) {
+        const int cn = chunk_at(k + 1);
+        fetch_tile<N, 128>(sC, in.C + grp * N + row_of(cn) * in.cs, in.cs, rows_in(cn), tid);
+        copy_commit();
+      }
+    }
+
+    // the state's decay, then both products that read x
+    const float all = m.all;
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st[i][e] *= all;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t x[4];  // (p, p + 8) x (j, j + 8) of x^T
+      ldsm4t(tile_at<64>(sX, 16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)), x);
+      if constexpr (LEAVE == kY) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i < j) continue;  // above the diagonal
+          uint32_t a[4];
+          ldsm4(block_rows<64>(sM, 16 * i, 2 * j, lane), a);
+          mma16816(yv[i][0], a, x[0], x[2]);
+          mma16816(yv[i][1], a, x[1], x[3]);
+          ldsm4(block_rows<64>(sM + 8192, 16 * i, 2 * j, lane), a);
+          mma16816(yv[i][0], a, x[0], x[2]);
+          mma16816(yv[i][1], a, x[1], x[3]);
+        }
+      }
+      const float *wv = REV ? m.gam : m.w;
+      const float2 wa = *reinterpret_cast<const float2 *>(wv + 16 * j + 2 * q);
+      const float2 wb = *reinterpret_cast<const float2 *>(wv + 16 * j + 8 + 2 * q);
+      uint32_t u0[4], u1[4], u2[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        bf2_get(x[e], lo, hi);
+        const float2 w = e < 2 ? wa : wb;
+        split3(lo * w.x, hi * w.y, u0[e], u1[e], u2[e]);
+      }
+#pragma unroll
+      for (int i = 0; i < N / 16; ++i) {
+        uint32_t b[4];
+        ldsm4t(block_rows<N>(sB, 16 * j, 2 * i, lane), b);  // (j, j + 8) x (n, n + 8)
+        mma16816(st[2 * i], u0, b[0], b[1]);
+        mma16816(st[2 * i + 1], u0, b[2], b[3]);
+        mma16816(st[2 * i], u1, b[0], b[1]);
+        mma16816(st[2 * i + 1], u1, b[2], b[3]);
+        mma16816(st[2 * i], u2, b[0], b[1]);
+        mma16816(st[2 * i + 1], u2, b[2], b[3]);
+      }
+    }
+    if (LEAVE == kEnds) run_decay *= all;
+    if constexpr (LEAVE == kY) {
+      const int n = rows_in(c);
+      const long long row0 = row_of(c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 16 * i + g + 8 * e;
+            uint32_t xr;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(xr) : "r"(tile_at<64>(sX, r, 2 * warp + j) + q * 4));
+            float xa, xb;
+            bf2_get(xr, xa, xb);
+            if (r < n)
+              *reinterpret_cast<uint32_t *>(y + ((row0 + r) * in.H + h) * in.P + pt * 64 + warp * 16 + 8 * j + 2 * q) =
+                  bf2_set(fmaf(Dh, xa, yv[i][j][2 * e]), fmaf(Dh, xb, yv[i][j][2 * e + 1]));
+          }
+    }
+    if (k + 1 < total) {
+      const int cn = chunk_at(k + 1);
+      if (warp == ((k + 1) & 3)) decays_of(in, row_of(cn), rows_in(cn), h, A, bias, dec[(k + 1) & 1]);
+      __syncthreads();  // B, x and M are free
+      fetch_tile<N, 128>(sB, Bp + row_of(cn) * Bs, Bs, rows_in(cn), tid);
+      fetch_tile<64, 128>(sX, Xp + row_of(cn) * Xs, Xs, rows_in(cn), tid);
+      copy_commit();
+    }
+  }
+
+  float *dst = nullptr;
+  if (LEAVE == kEnds) {
+    dst = ends.state + (slot * in.H + h) * np + p0;
+    if (tid == 0 && pt == 0) ends.decay[slot * in.H + h] = run_decay;
+  } else if (last_seg && out_state) {
+    dst = out_state + ((long long)t.seq * in.H + h) * np + p0;
+  }
+  if (dst) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        dst[(8 * i + 2 * q + (e & 1)) * (long long)in.P + (e >> 1) * 8] = st[i][e];
+  }
+}
+
+}  // namespace scan
+}  // namespace gdn

@@ -85,6 +85,22 @@ def test_packed(cuda_lib, lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,n,N", [(577, 1, 128), (1000, 2, 64), ((600, 0, 321, 64, 1), 5, 128)])
+def test_long_sequences_of_few_heads(cuda_lib, T, n, N, dtype):
+    """Few heads and many chunks: the sequences are cut into runs."""
+    check(cuda_lib, T, n, 2, 64, 1, N, dtype, state=True)
+
+
+def test_state_in_place_over_runs(cuda_lib):
+    (x, raw, A, B, C), D, bias, st, _, _ = make(12, (2, 900), 2, 128, 1, 64, BF16, 2, True)
+    y0, s0 = cuda_lib.gdn_scan_prefill(x, raw, A, B, C, D=D, dt_bias=bias, state_in=st)
+    for _ in range(20):
+        s, y = st.clone(), torch.empty_like(y0)
+        cuda_lib.gdn_scan_prefill_into(x, raw, A, B, C, D, bias, s, None, y, s)
+        assert torch.equal(s, s0) and torch.equal(y, y0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_without_skip_and_bias(cuda_lib, dtype):
     check(cuda_lib, 70, 1, 2, 64, 1, 64, dtype, state=False, extra=False)
 
