@@ -2,6 +2,7 @@
 // and launches.
 #include "gdn_host.cuh"
 #include "gdn_layer.h"
+#include "gdn_scan_grad.cuh"
 #include "gdn_scan_mma.cuh"
 #include "gdn_scan_simt.cuh"
 
@@ -143,21 +144,59 @@ gdn_status decode(const Call &c, float *state, void *y, cudaStream_t st) {
   return launched();
 }
 
-// The gradient's workspace, every part a multiple of 16 bytes.
+// The gradient's workspace, every part a multiple of 16 bytes: the state at
+// every chunk's start and its adjoint at every chunk's end (fp32, or two bf16
+// pieces), dB and dC of every head (fp32) or of every share of a group's
+// heads (bf16, where there are several), the heads' parameters' parts of
+// every chunk, and for bf16 what runs of chunks hand over.
 struct Workspace {
+  Plan runs;
   long long slots, rows;
-  size_t states, adjoints, dB, dC, part, bytes;
+  int splits;
+  size_t states, adjoints, dB, dC, part, fwd, fwd_decay, rev, rev_decay, bytes;
 };
-Workspace workspace(int n_seq, int T, int H, int P, int N, bool packed) {
-  Workspace w;
+
+// CTAs that a group's heads are split over: each share forms C B^T again
+// (half a head's work), so the split is the one with the least work in a
+// row on one of the 148 SMs.
+int head_splits(long long chunks_groups, int R) {
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= R; ++s) {
+    if ((s - 1) * ((R + s - 1) / s) >= R) continue;  // an empty share
+    const double waves = (double)((chunks_groups * s + 147) / 148);
+    const double cost = waves * ((R + s - 1) / s + 0.5);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+Workspace workspace(int n_seq, int T, int H, int P, int G, int N, gdn_dtype dt, bool packed) {
+  Workspace w = {};
+  const bool mma = dt == GDN_DTYPE_BF16;
   w.slots = layer::slot_count(n_seq, T, kChunk, packed);
   w.rows = packed ? T : (long long)n_seq * T;
-  w.states = 0;
-  w.adjoints = w.states + (size_t)w.slots * H * N * P * 4;
-  w.dB = w.adjoints + (size_t)w.slots * H * N * P * 4;
-  w.dC = w.dB + (size_t)w.rows * H * N * 4;
-  w.part = w.dC + (size_t)w.rows * H * N * 4;
+  w.splits = mma ? head_splits(w.slots * G, H / G) : H / G;
+  const size_t states = (size_t)w.slots * H * N * P * 4;
+  const size_t sums = mma && w.splits == 1 ? 0 : (size_t)w.rows * G * w.splits * N * 4;
+  w.adjoints = states;
+  w.dB = w.adjoints + states;
+  w.dC = w.dB + sums;
+  w.part = w.dC + sums;
   w.bytes = w.part + (size_t)w.slots * H * 16;
+  if (mma) {
+    w.runs = plan(n_seq, T, H, P, N, packed);
+    if (w.runs.split) {
+      w.fwd = w.bytes;
+      w.fwd_decay = w.fwd + w.runs.decay;
+      w.rev = w.fwd + w.runs.copy;
+      w.rev_decay = w.rev + w.runs.decay;
+      w.bytes = w.rev + w.runs.copy;
+    }
+  }
   return w;
 }
 
@@ -170,42 +209,79 @@ struct Grads {
   float *dD, *dbias, *dstate_in;
 };
 
-template <typename T, int N, int P>
-gdn_status backward_shape(const Call &c, const Grads &g, char *ws, unsigned *err, cudaStream_t st) {
-  const In<T> in = typed<T>(c);
-  const Workspace w = workspace(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr);
-  float *states = reinterpret_cast<float *>(ws + w.states);
-  float *adjoints = reinterpret_cast<float *>(ws + w.adjoints);
-  float *dBh = reinterpret_cast<float *>(ws + w.dB), *dCh = reinterpret_cast<float *>(ws + w.dC);
-  float *part = reinterpret_cast<float *>(ws + w.part);
-  const T *dy = static_cast<const T *>(g.dy);
-  sweep_kernel<T, N, kStates><<<units(c), 256, 0, st>>>(in, nullptr, nullptr, nullptr, nullptr, states, err);
-  sweep_kernel<T, N, kAdjoint><<<units(c), 256, 0, st>>>(in, dy, g.dstate_out, nullptr, g.dstate_in,
-                                                         adjoints, err);
-  auto kern = chunk_grad_kernel<T, N, P>;
-  constexpr size_t smem = ChunkLayout<N, P>::bytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return GDN_ERR_CUDA;
-  kern<<<(unsigned)(w.slots * c.H), 256, smem, st>>>(in, dy, states, adjoints,
-                                                     static_cast<T *>(g.dx), static_cast<T *>(g.draw),
-                                                     dBh, dCh, part);
-  const long long total = w.rows * c.G * N;
-  if (total > 0) {
+template <typename T>
+gdn_status sums(const Call &c, const Grads &g, const Workspace &w, char *ws, bool heads, cudaStream_t st) {
+  const long long total = w.rows * c.G * c.N;
+  if (heads && total > 0) {
     const long long want = (total + 255) / 256;
     head_sum_kernel<T><<<(unsigned)(want < 148 * 16 ? want : 148 * 16), 256, 0, st>>>(
-        dBh, dCh, total, c.H / c.G, N, static_cast<T *>(g.dB), static_cast<T *>(g.dC));
+        reinterpret_cast<float *>(ws + w.dB), reinterpret_cast<float *>(ws + w.dC), total, w.splits,
+        c.N, static_cast<T *>(g.dB), static_cast<T *>(g.dC));
   }
-  head_param_kernel<<<c.H, 128, 0, st>>>(part, w.slots, c.H, g.dA, g.dD, g.dbias);
+  head_param_kernel<<<c.H, 128, 0, st>>>(reinterpret_cast<float *>(ws + w.part), w.slots, c.H, g.dA,
+                                         g.dD, g.dbias);
   return launched();
 }
 
-template <typename T>
-gdn_status backward(const Call &c, const Grads &g, char *ws, unsigned *err, cudaStream_t st) {
-  if (c.N == 128)
-    return c.P == 128 ? backward_shape<T, 128, 128>(c, g, ws, err, st)
-                      : backward_shape<T, 128, 64>(c, g, ws, err, st);
-  return c.P == 128 ? backward_shape<T, 64, 128>(c, g, ws, err, st)
-                    : backward_shape<T, 64, 64>(c, g, ws, err, st);
+template <int N, int P>
+gdn_status backward_f32(const Call &c, const Grads &g, char *ws, unsigned *err, cudaStream_t st) {
+  const In<float> in = typed<float>(c);
+  const Workspace w = workspace(c.n_seq, c.T, c.H, c.P, c.G, c.N, GDN_DTYPE_F32, c.cu != nullptr);
+  float *states = reinterpret_cast<float *>(ws + w.states);
+  float *adjoints = reinterpret_cast<float *>(ws + w.adjoints);
+  const float *dy = static_cast<const float *>(g.dy);
+  sweep_kernel<float, N, kStates><<<units(c), 256, 0, st>>>(in, nullptr, nullptr, nullptr, nullptr, states, err);
+  sweep_kernel<float, N, kAdjoint><<<units(c), 256, 0, st>>>(in, dy, g.dstate_out, nullptr, g.dstate_in,
+                                                             adjoints, err);
+  auto kern = chunk_grad_kernel<float, N, P>;
+  constexpr size_t smem = ChunkLayout<N, P>::bytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  kern<<<(unsigned)(w.slots * c.H), 256, smem, st>>>(
+      in, dy, states, adjoints, static_cast<float *>(g.dx), static_cast<float *>(g.draw),
+      reinterpret_cast<float *>(ws + w.dB), reinterpret_cast<float *>(ws + w.dC),
+      reinterpret_cast<float *>(ws + w.part));
+  return sums<float>(c, g, w, ws, true, st);
+}
+
+template <int N, int P>
+gdn_status backward_mma(const Call &c, const Grads &g, char *ws, unsigned *err, cudaStream_t st) {
+  using T = __nv_bfloat16;
+  const In<T> in = typed<T>(c);
+  const Workspace w = workspace(c.n_seq, c.T, c.H, c.P, c.G, c.N, GDN_DTYPE_BF16, c.cu != nullptr);
+  const T *dy = static_cast<const T *>(g.dy);
+  const Ends fwd{reinterpret_cast<float *>(ws + w.fwd), reinterpret_cast<float *>(ws + w.fwd_decay)};
+  const Ends rev{reinterpret_cast<float *>(ws + w.rev), reinterpret_cast<float *>(ws + w.rev_decay)};
+  uint32_t *states = reinterpret_cast<uint32_t *>(ws + w.states);
+  uint32_t *adjoints = reinterpret_cast<uint32_t *>(ws + w.adjoints);
+  gdn_status s;
+  if (w.runs.split) {
+    if ((s = sweep<N, kEnds, false>(in, w.runs, nullptr, nullptr, fwd, nullptr, nullptr, nullptr, err, st)) != GDN_OK ||
+        (s = sweep<N, kEnds, true>(in, w.runs, dy, nullptr, rev, nullptr, nullptr, nullptr, err, st)) != GDN_OK)
+      return s;
+  }
+  if ((s = sweep<N, kChunks, false>(in, w.runs, nullptr, c.state_in, fwd, nullptr, nullptr, states, err, st)) != GDN_OK ||
+      (s = sweep<N, kChunks, true>(in, w.runs, dy, g.dstate_out, rev, nullptr, g.dstate_in, adjoints, err, st)) != GDN_OK)
+    return s;
+  auto kern = chunk_grad_mma_kernel<N, P>;
+  constexpr int smem = (int)GradSmem<N, P>::bytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  const GroupOut out{static_cast<T *>(g.dB), static_cast<T *>(g.dC), reinterpret_cast<float *>(ws + w.dB),
+                     reinterpret_cast<float *>(ws + w.dC)};
+  kern<<<(unsigned)(w.slots * c.G * w.splits), 256, smem, st>>>(
+      in, dy, reinterpret_cast<T *>(states), reinterpret_cast<T *>(adjoints), w.splits,
+      static_cast<T *>(g.dx), static_cast<T *>(g.draw), out, reinterpret_cast<float *>(ws + w.part));
+  if ((s = launched()) != GDN_OK) return s;
+  return sums<T>(c, g, w, ws, w.splits > 1, st);
+}
+
+gdn_status backward(const Call &c, gdn_dtype dt, const Grads &g, char *ws, unsigned *err, cudaStream_t st) {
+#define GDN_BWD(FN)                                                                      \
+  (c.N == 128 ? (c.P == 128 ? FN<128, 128>(c, g, ws, err, st) : FN<128, 64>(c, g, ws, err, st)) \
+              : (c.P == 128 ? FN<64, 128>(c, g, ws, err, st) : FN<64, 64>(c, g, ws, err, st)))
+  return dt == GDN_DTYPE_BF16 ? GDN_BWD(backward_mma) : GDN_BWD(backward_f32);
+#undef GDN_BWD
 }
 
 }  // namespace scan
@@ -266,7 +342,7 @@ size_t gdn_scan_backward_workspace_bytes(int n_seq, int T, int H, int P, int G, 
   const scan::Call c{nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, nullptr, nullptr, nullptr,
                      nullptr, nullptr, 0, T, H, P, G, N};
   if (n_seq <= 0 || scan::check(c, dtype, false) != GDN_OK) return 0;
-  return scan::workspace(n_seq, T, H, P, N, packed != 0).bytes;
+  return scan::workspace(n_seq, T, H, P, G, N, dtype, packed != 0).bytes;
 }
 
 gdn_status gdn_scan_backward(const void *x, int64_t x_stride, const void *dt_raw,
@@ -302,8 +378,7 @@ gdn_status gdn_scan_backward(const void *x, int64_t x_stride, const void *dt_raw
   if (cu_seqlens && (s = error_word(&err)) != GDN_OK) return s;
   const scan::Grads g{dy, dstate_out, dx, ddt, dA, dB, dC, dD, ddt_bias, dstate_in};
   char *ws = static_cast<char *>(workspace);
-  return dtype == GDN_DTYPE_F32 ? scan::backward<float>(c, g, ws, err, st)
-                                : scan::backward<__nv_bfloat16>(c, g, ws, err, st);
+  return scan::backward(c, dtype, g, ws, err, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,492 @@
+// Gradient of the scan's chunks for bf16 inputs on the tensor cores: the
+// algebra of chunk_grad_kernel with mma.sync products of bf16 pieces (pairs
+// for M, W, the states and the adjoints: 2^-17 relative).
+//
+// A CTA of eight warps takes one chunk and a range of one group's heads.
+// S = C B^T is formed once; dB and dC are summed over the heads in the
+// accumulators, so that neither leaves the SM before it is whole (with the
+// heads split over several CTAs, their fp32 parts are added afterwards in
+// order).  Bound by the legacy tensor rate (1024 multiply-adds a clock and
+// SM) of some six million multiply-adds a head and chunk at N = 128, P = 64.
+#pragma once
+
+#include "gdn_scan_mma.cuh"
+
+namespace gdn {
+namespace scan {
+
+template <int N, int P>
+struct GradSmem {
+  static constexpr uint32_t C = 0, B = C + 64 * N * 2;
+  static constexpr uint32_t X = B + 64 * N * 2;            // P / 64 tiles of 64 x 64
+  static constexpr uint32_t Y = X + 64 * P * 2;
+  static constexpr uint32_t H = Y + 64 * P * 2;            // hi, lo: [64 p][N]
+  static constexpr uint32_t G = H + 2 * 64 * N * 2;
+  static constexpr uint32_t M = G + 2 * 64 * N * 2;        // hi, lo
+  static constexpr uint32_t W = M + 2 * 64 * 64 * 2;
+  static constexpr uint32_t Z = W + 2 * 64 * 64 * 2;       // fp32 [64][65]
+  static constexpr uint32_t V = (Z + 64 * 65 * 4 + 15) / 16 * 16;
+  // row sums by warp column: r, q, x . du (4 each), Z block sums [4][64], l, gh and dD by warp
+  struct Rows {
+    float r[4][64], q[4][64], xdu[4][64], zb[4][64], l[64], gh[8], dD[8];
+  };
+  static constexpr uint32_t D = V + (sizeof(Rows) + 15) / 16 * 16;
+  static constexpr uint32_t bytes = D + 2 * sizeof(Decays);
+};
+
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// dst: bf16 [tokens, G, N], or with parts fp32 [tokens, G, splits, N].
+struct GroupOut {
+  __nv_bfloat16 *b, *c;
+  float *pb, *pc;
+};
+
+template <int N, int P>
+__global__ void __launch_bounds__(256, 1)
+chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ dy,
+                      const __nv_bfloat16 *__restrict__ states,
+                      const __nv_bfloat16 *__restrict__ adjoints, int splits,
+                      __nv_bfloat16 *__restrict__ dx, __nv_bfloat16 *__restrict__ draw, GroupOut out,
+                      float *__restrict__ part) {
+  using L = GradSmem<N, P>;
+  constexpr int kPT = P / 64, kJ = N / 64;  // n16 blocks of a warp's share of N
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t base = smem_at(smem);
+  const uint32_t sC = base + L::C, sB = base + L::B, sX = base + L::X, sY = base + L::Y;
+  const uint32_t sH = base + L::H, sG = base + L::G, sM = base + L::M, sW = base + L::W;
+  float *sZ = reinterpret_cast<float *>(smem + L::Z);
+  typename L::Rows &rs = *reinterpret_cast<typename L::Rows *>(smem + L::V);
+  Decays *dec = reinterpret_cast<Decays *>(smem + L::D);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int sp = blockIdx.x % splits, grp = blockIdx.x / splits % in.G;
+  const long long slot = blockIdx.x / splits / in.G;
+  const int R = in.H / in.G, per = (R + splits - 1) / splits;
+  const int h0 = grp * R + min(R, sp * per), h1 = grp * R + min(R, (sp + 1) * per);
+  const Tile t = find_tile(in.cu, in.n_seq, in.T_, 64, slot);
+  const int n = t.seq < 0 ? 0 : (int)min(64LL, t.len - (long long)t.tile * 64);
+  if (n <= 0) {
+    for (int h = h0 + tid; h < h1; h += 256)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) part[(slot * in.H + h) * 4 + k] = 0.0f;
+    return;
+  }
+  const long long row0 = t.start + (long long)t.tile * 64;
+  const long long np = (long long)N * in.P;
+
+  auto fetch_states = [&](int h, int pt) {
+    const __nv_bfloat16 *s = states + (slot * in.H + h) * 2 * np + (long long)pt * 64 * N;
+    const __nv_bfloat16 *a = adjoints + (slot * in.H + h) * 2 * np + (long long)pt * 64 * N;
+    fetch_tile<N, 256>(sH, s, N, 64, tid);
+    fetch_tile<N, 256>(sH + 64 * N * 2, s + np, N, 64, tid);
+    fetch_tile<N, 256>(sG, a, N, 64, tid);
+    fetch_tile<N, 256>(sG + 64 * N * 2, a + np, N, 64, tid);
+  };
+  auto fetch_head = [&](int h) {
+#pragma unroll
+    for (int pt = 0; pt < kPT; ++pt) {
+      fetch_tile<64, 256>(sX + pt * 8192, in.x + row0 * in.xs + (long long)h * P + pt * 64, in.xs, n, tid);
+      fetch_tile<64, 256>(sY + pt * 8192, dy + (row0 * in.H + h) * P + pt * 64, (long long)in.H * P, n, tid);
+    }
+    fetch_states(h, 0);
+  };
+  fetch_tile<N, 256>(sB, in.B + row0 * in.bs + grp * N, in.bs, n, tid);
+  fetch_tile<N, 256>(sC, in.C + row0 * in.cs + grp * N, in.cs, n, tid);
+  if (h0 < h1) {
+    fetch_head(h0);
+    if (warp == 0) decays_of(in, row0, n, h0, in.A[h0], in.bias ? in.bias[h0] : 0.0f, dec[0]);
+  }
+  copy_commit();
+
+  // S for this warp's 16 rows and 32 columns, unless all lie above the diagonal
+  const int sr = 16 * (warp >> 1), sc = 32 * (warp & 1);
+  const bool lower = sc <= sr + 15;
+  const int gr = 32 * (warp >> 2), gc = (N / 4) * (warp & 3);  // rows, columns of dB and dC
+  const int ur = gr, uc = 16 * (warp & 3);                     // of du
+  float S[4][4], aB[2][2 * kJ][4], aC[2][2 * kJ][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[i][e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2 * kJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) aB[i][j][e] = aC[i][j][e] = 0.0f;
+
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    const Decays &m = dec[(h - h0) & 1];
+    copy_wait<0>();
+    __syncthreads();
+    if (h == h0 && lower) {
+#pragma unroll
+      for (int kk = 0; kk < N / 16; ++kk) {
+        uint32_t a[4], b[4];
+        ldsm4(block_rows<N>(sC, sr, 2 * kk, lane), a);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          ldsm4(block_cols<N>(sB, sc + 16 * j, 2 * kk, lane), b);
+          mma16816(S[2 * j], a, b[0], b[1]);
+          mma16816(S[2 * j + 1], a, b[2], b[3]);
+        }
+      }
+    }
+    // K = dy x^T, then M, W and Z
+    float dD = 0.0f;
+    if (lower) {
+      float K[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) K[i][e] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < P / 16; ++kk) {
+        const uint32_t tx = sX + (kk / 4) * 8192, ty = sY + (kk / 4) * 8192;
+        uint32_t a[4], b[4];
+        ldsm4(block_rows<64>(ty, sr, 2 * (kk % 4), lane), a);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          ldsm4(block_cols<64>(tx, sc + 16 * j, 2 * (kk % 4), lane), b);
+          mma16816(K[2 * j], a, b[0], b[1]);
+          mma16816(K[2 * j + 1], a, b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = sr + g + 8 * e;
+        const float hr = m.hi[r], lr = m.lo[r];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = sc + 8 * j + 2 * q;
+          float mv[2], wv[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float k = K[j][2 * e + u], s = S[j][2 * e + u];
+            const float d = r >= c + u ? exp2_fast((hr - m.hi[c + u]) + (lr - m.lo[c + u])) : 0.0f;
+            if (r == c + u) dD += k;
+            mv[u] = s * d;
+            wv[u] = k * d * m.dt[c + u];
+            sZ[r * 65 + c + u] = s * wv[u];
+          }
+          uint32_t hi, lo;
+          const uint32_t at = (uint32_t)r * 128 + ((uint32_t)((c >> 3) ^ (r & 7)) << 4) + q * 4;
+          split2(mv[0], mv[1], hi, lo);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sM + at), "r"(hi) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sM + 8192 + at), "r"(lo) : "memory");
+          split2(wv[0], wv[1], hi, lo);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + at), "r"(hi) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + 8192 + at), "r"(lo) : "memory");
+        }
+      }
+    } else {  // above the diagonal: Z alone is read there
+      for (int i = lane; i < 16 * 32; i += 32) sZ[(sr + i / 32) * 65 + sc + i % 32] = 0.0f;
+    }
+    dD = warp_sum(dD);
+    if (lane == 0) rs.dD[warp] = dD;
+    float gh = 0.0f;
+    __syncthreads();
+
+    // Z summed from each 16-row block's last row up
+    {
+      const int c = tid & 63, b = tid >> 6;
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 15; i >= 0; --i) {
+        s += sZ[(16 * b + i) * 65 + c];
+        sZ[(16 * b + i) * 65 + c] = s;
+      }
+      rs.zb[b][c] = s;
+    }
+    // what needs no state: dC += W B, dB += W^T C
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t b[kJ][4];
+      const bool need_c = kk <= gr / 16 + 1, need_b = kk >= gr / 16;
+      if (need_c) {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) ldsm4t(block_rows<N>(sB, 16 * kk, gc / 8 + 2 * j, lane), b[j]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (kk > gr / 16 + i) continue;
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece) {
+            uint32_t a[4];
+            ldsm4(block_rows<64>(sW + piece * 8192, gr + 16 * i, 2 * kk, lane), a);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+              mma16816(aC[i][2 * j], a, b[j][0], b[j][1]);
+              mma16816(aC[i][2 * j + 1], a, b[j][2], b[j][3]);
+            }
+          }
+        }
+      }
+      if (need_b) {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) ldsm4t(block_rows<N>(sC, 16 * kk, gc / 8 + 2 * j, lane), b[j]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (kk < gr / 16 + i) continue;
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece) {
+            uint32_t a[4];
+            ldsm4t(block_cols<64>(sW + piece * 8192, 16 * kk, (gr + 16 * i) / 8, lane), a);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+              mma16816(aB[i][2 * j], a, b[j][0], b[j][1]);
+              mma16816(aB[i][2 * j + 1], a, b[j][2], b[j][3]);
+            }
+          }
+        }
+      }
+    }
+    float rsum[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, qsum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    float xsum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    const float Dh = in.D ? in.D[h] : 0.0f;
+#pragma unroll 1
+    for (int pt = 0; pt < kPT; ++pt) {
+      const uint32_t tX = sX + pt * 8192, tY = sY + pt * 8192;
+      if (pt > 0) {
+        __syncthreads();  // the first tile's states have been read
+        fetch_states(h, pt);
+        copy_commit();
+        copy_wait<0>();
+        __syncthreads();
+      }
+      // dC += e^{c_i} dy H0 and its products with C; then dB with x and G
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const uint32_t tA = side ? tX : tY, tS = side ? sG : sH, tO = side ? sB : sC;
+        float T[2][2 * kJ][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2 * kJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) T[i][j][e] = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ldsm4(block_rows<64>(tA, gr + 16 * i, 2 * kk, lane), a[i]);
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+              uint32_t b[4];
+              ldsm4t(block_rows<N>(tS + piece * 64 * N * 2, 16 * kk, gc / 8 + 2 * j, lane), b);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                mma16816(T[i][2 * j], a[i], b[0], b[1]);
+                mma16816(T[i][2 * j + 1], a[i], b[2], b[3]);
+              }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = gr + 16 * i + g + 8 * e;
+            const float f = side ? m.w[r] : m.gam[r];
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 2 * kJ; ++j) {
+              uint32_t o;
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o) : "r"(tile_at<N>(tO, r, gc / 8 + j) + q * 4));
+              float oa, ob;
+              bf2_get(o, oa, ob);
+              const float ta = f * T[i][j][2 * e], tb = f * T[i][j][2 * e + 1];
+              s = fmaf(oa, ta, fmaf(ob, tb, s));
+              if (side) {
+                aB[i][j][2 * e] += ta;
+                aB[i][j][2 * e + 1] += tb;
+              } else {
+                aC[i][j][2 * e] += ta;
+                aC[i][j][2 * e + 1] += tb;
+              }
+            }
+            if (side) qsum[i][e] += s;
+            else rsum[i][e] += s;
+          }
+      }
+      // du = M^T dy + e^{c_n - c_j} B G^T, dx, x . du
+      {
+        float U[2][2][4], T[2][2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) U[i][j][e] = T[i][j][e] = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk < ur / 16) continue;
+          uint32_t b[4];
+          ldsm4t(block_rows<64>(tY, 16 * kk, uc / 8, lane), b);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (kk < ur / 16 + i) continue;
+#pragma unroll
+            for (int piece = 0; piece < 2; ++piece) {
+              uint32_t a[4];
+              ldsm4t(block_cols<64>(sM + piece * 8192, 16 * kk, (ur + 16 * i) / 8, lane), a);
+              mma16816(U[i][0], a, b[0], b[1]);
+              mma16816(U[i][1], a, b[2], b[3]);
+            }
+          }
+        }
+#pragma unroll
+        for (int kk = 0; kk < N / 16; ++kk) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ldsm4(block_rows<N>(sB, ur + 16 * i, 2 * kk, lane), a[i]);
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece) {
+            uint32_t b[4];
+            ldsm4(block_cols<N>(sG + piece * 64 * N * 2, uc, 2 * kk, lane), b);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              mma16816(T[i][0], a[i], b[0], b[1]);
+              mma16816(T[i][1], a[i], b[2], b[3]);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = ur + 16 * i + g + 8 * e;
+            const float d = m.del[r], dt = m.dt[r];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t xr, yr;
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(xr) : "r"(tile_at<64>(tX, r, uc / 8 + j) + q * 4));
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(yr) : "r"(tile_at<64>(tY, r, uc / 8 + j) + q * 4));
+              float xa, xb, ya, yb;
+              bf2_get(xr, xa, xb);
+              bf2_get(yr, ya, yb);
+              const float ua = fmaf(d, T[i][j][2 * e], U[i][j][2 * e]);
+              const float ub = fmaf(d, T[i][j][2 * e + 1], U[i][j][2 * e + 1]);
+              xsum[i][e] = fmaf(xa, ua, fmaf(xb, ub, xsum[i][e]));
+              if (r < n)
+                *reinterpret_cast<uint32_t *>(dx + ((row0 + r) * in.H + h) * P + pt * 64 + uc + 8 * j + 2 * q) =
+                    bf2_set(fmaf(dt, ua, Dh * ya), fmaf(dt, ub, Dh * yb));
+            }
+          }
+      }
+      // <G, H0>
+      for (int i = tid; i < 64 * N / 8; i += 256) {
+        const uint32_t at = (uint32_t)i * 16;
+        uint32_t a[4], b[4], c[4], d[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(sH + at));
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]) : "r"(sH + 64 * N * 2 + at));
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(sG + at));
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(sG + 64 * N * 2 + at));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float p0, p1, l0, l1, g0, g1, k0, k1;
+          bf2_get(a[e], p0, p1);
+          bf2_get(b[e], l0, l1);
+          bf2_get(c[e], g0, g1);
+          bf2_get(d[e], k0, k1);
+          gh = fmaf(p0 + l0, g0 + k0, fmaf(p1 + l1, g1 + k1, gh));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = gr + 16 * i + g + 8 * e;
+        const float a = quad_sum(rsum[i][e]), b = quad_sum(qsum[i][e]), c = quad_sum(xsum[i][e]);
+        if (q == 0) {
+          rs.r[warp & 3][r] = a;
+          rs.q[warp & 3][r] = b;
+          rs.xdu[warp & 3][r] = c;
+        }
+      }
+    gh = warp_sum(gh);
+    if (lane == 0) rs.gh[warp] = gh;
+    __syncthreads();  // every tile of this head has been read
+    if (h + 1 < h1) {
+      fetch_head(h + 1);
+      copy_commit();
+      if (warp == 7)
+        decays_of(in, row0, n, h + 1, in.A[h + 1], in.bias ? in.bias[h + 1] : 0.0f, dec[(h + 1 - h0) & 1]);
+    }
+    // l_t, four threads a token
+    {
+      const int tt = tid >> 2, b = tid & 3;
+      float s = 0.0f;
+      for (int c = 16 * b; c < min(16 * b + 16, tt); ++c) {
+        s += sZ[tt * 65 + c];
+        for (int k = tt / 16 + 1; k < 4; ++k) s += rs.zb[k][c];
+        s += (rs.q[0][c] + rs.q[1][c]) + (rs.q[2][c] + rs.q[3][c]);
+      }
+      for (int c = max(16 * b, tt); c < 16 * b + 16; ++c)
+        s += (rs.r[0][c] + rs.r[1][c]) + (rs.r[2][c] + rs.r[3][c]);
+      s = quad_sum(s);
+      if (b == 0) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += rs.gh[w];
+        rs.l[tt] = fmaf(m.all, v, s);
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const float A = in.A[h];
+      float dA = 0.0f, db = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = lane + 32 * k;
+        if (r < n) {
+          const float x = (rs.xdu[0][r] + rs.xdu[1][r]) + (rs.xdu[2][r] + rs.xdu[3][r]);
+          const float d = fmaf(A, rs.l[r], x) * m.sig[r];
+          draw[(row0 + r) * in.H + h] = __float2bfloat16_rn(d);
+          dA = fmaf(m.dt[r], rs.l[r], dA);
+          db += d;
+        }
+      }
+      dA = warp_sum(dA);
+      db = warp_sum(db);
+      if (lane == 0) {
+        float *po = part + (slot * in.H + h) * 4;
+        float d = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) d += rs.dD[w];
+        po[0] = dA;
+        po[1] = d;
+        po[2] = db;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = gr + 16 * i + g + 8 * e;
+      if (r >= n) continue;
+      const long long row = (row0 + r) * in.G + grp;
+#pragma unroll
+      for (int j = 0; j < 2 * kJ; ++j) {
+        const int c = gc + 8 * j + 2 * q;
+        if (splits == 1) {
+          *reinterpret_cast<uint32_t *>(out.b + row * N + c) = bf2_set(aB[i][j][2 * e], aB[i][j][2 * e + 1]);
+          *reinterpret_cast<uint32_t *>(out.c + row * N + c) = bf2_set(aC[i][j][2 * e], aC[i][j][2 * e + 1]);
+        } else {
+          const long long at = (row * splits + sp) * N + c;
+          *reinterpret_cast<float2 *>(out.pb + at) = make_float2(aB[i][j][2 * e], aB[i][j][2 * e + 1]);
+          *reinterpret_cast<float2 *>(out.pc + at) = make_float2(aC[i][j][2 * e], aC[i][j][2 * e + 1]);
+        }
+      }
+    }
+}
+
+}  // namespace scan
+}  // namespace gdn

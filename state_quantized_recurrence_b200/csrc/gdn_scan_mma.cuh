@@ -111,10 +111,13 @@ struct alignas(16) Decays {  // two of them lie side by side and are read in pai
   float w[64];            // del * dt
   float all;              // e^{c_n}: the decay of the state over the chunk
 };
+// 2^v with its subnormals (the decays of whole chunks reach them).
 __device__ __forceinline__ float exp2_of(double v) {
   const float h = (float)v;
   const float l = (float)(v - (double)h);
-  return exp2_fast(h) * fmaf(l, 0.693147181f, 1.0f);
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(h));
+  return r * fmaf(l, 0.693147181f, 1.0f);
 }
 // By one warp, two tokens a lane; tokens past n have step 0 and decay 1.
 __device__ __forceinline__ void decays_of(const In<__nv_bfloat16> &in, long long row0, int n, int h,

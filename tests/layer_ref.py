@@ -161,15 +161,16 @@ def half_step(dtype):
     return torch.finfo(dtype).eps / 2
 
 
-def within(got, ref, mag, terms, name, extra=0.0):
+def within(got, ref, mag, terms, name, extra=0.0, floor=0.0):
     """Every element within one rounding to its type plus `terms` fp32
     roundings (and `extra`, relative) of the magnitudes that were added.
-    Values below the type's normal range carry half its smallest step."""
+    Values below the type's normal range carry half its smallest step, and
+    `floor` stands for one that the call's own arithmetic has."""
     dtype = got.dtype
     g, ref, mag = got.detach().double().cpu(), ref, mag
     assert g.shape == ref.shape, (name, g.shape, ref.shape)
     tiny = torch.finfo(dtype).tiny
-    tol = half_step(dtype) * (ref.abs() + tiny) + (terms * U + extra) * (mag + tiny)
+    tol = half_step(dtype) * (ref.abs() + tiny) + (terms * U + extra) * (mag + tiny) + floor
     bad = ~((g - ref).abs() <= tol)
     assert not bad.any(), "%s: %d of %d off, worst %.3g of its bound" % (
         name, int(bad.sum()), bad.numel(), float(((g - ref).abs() / tol).max()))
