@@ -8,7 +8,7 @@ from typing import Optional
 
 import torch
 
-from ._binding import GDN_DTYPE, GdnError, _need, _ptr, _stream, lib
+from ._binding import GDN_DTYPE, GdnError, _need, lib
 
 GDN_ACT = {None: 0, "none": 0, "silu": 1}
 GDN_NORM_OUT = {"none": 0, "fp8_row": 1, "int8_g32": 2, "int8_g16": 3, "int8_g64": 4}
@@ -39,47 +39,84 @@ _declare()
 
 
 # ------------------------------------------------------------------ checks ----
+# Single-token calls are as short as their launch: messages are formatted
+# only when they are raised, and the device is switched only when it differs.
 def _device(*ts) -> torch.device:
     dev = None
     for t in ts:
-        if t is not None:
-            _need(t.is_cuda, "tensors must be CUDA tensors")
-            dev = dev or t.device
-            _need(t.device == dev, f"tensors on different devices ({dev} and {t.device})")
+        if t is None:
+            continue
+        d = t.device
+        if dev is None:
+            if d.type != "cuda":
+                raise ValueError("tensors must be CUDA tensors")
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors on different devices ({dev} and {d})")
     return dev
 
 
-def _dense(*ts) -> None:
-    for t in ts:
-        _need(t is None or t.is_contiguous(), "outputs, states and gradients must be contiguous")
+def _call(f, name: str, dev: torch.device, stream, *args) -> None:
+    """The C call on ``dev`` and on ``stream`` (default: the current stream
+    of ``dev``)."""
+    if dev.index == torch.cuda.current_device():
+        status = f(*args, _handle(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, _handle(stream, dev))
+    if status != 0:
+        raise GdnError(status, name)
+
+
+# The current stream's handle without a Stream object around it, where this
+# torch has the call.
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _handle(stream, dev) -> int:
+    return _current_raw(dev.index) if stream is None else stream.cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _f32(shape, name, t) -> None:
-    _need(t is None or (t.dtype == torch.float32 and tuple(t.shape) == tuple(shape)
-                        and t.is_contiguous()),
-          f"{name} must be contiguous fp32 {list(shape)}")
+    if t is not None and not (t.dtype == torch.float32 and t.shape == shape
+                              and t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous fp32 {list(shape)}")
 
 
 def _token_stride(t: torch.Tensor, inner: int, name: str) -> int:
     """Elements between consecutive tokens of ``t``, whose last ``inner``
     dimensions are one token's contiguous row and whose leading ones are the
     tokens, equally far apart (a slice of a projection's output qualifies)."""
-    row = 1
-    for d in range(t.dim() - 1, t.dim() - 1 - inner, -1):
-        _need(t.shape[d] == 1 or t.stride(d) == row, f"{name}: a token's row must be contiguous")
-        row *= t.shape[d]
+    shape, strides = t.shape, t.stride()
+    row, d = 1, len(shape) - 1
+    for d in range(len(shape) - 1, len(shape) - 1 - inner, -1):
+        if shape[d] != 1 and strides[d] != row:
+            raise ValueError(f"{name}: a token's row must be contiguous")
+        row *= shape[d]
     stride, span = None, 1
-    for d in range(t.dim() - 1 - inner, -1, -1):
-        if t.shape[d] == 1:
+    for d in range(len(shape) - 1 - inner, -1, -1):
+        if shape[d] == 1:
             continue
         if stride is None:
-            stride = t.stride(d)
-        _need(t.stride(d) == stride * span, f"{name}: tokens must be equally far apart")
-        span *= t.shape[d]
-    if t.numel() == 0 or stride is None:
+            stride = strides[d]
+        if strides[d] != stride * span:
+            raise ValueError(f"{name}: tokens must be equally far apart")
+        span *= shape[d]
+    if stride is None or row == 0 or span == 0:
         return row
-    _need(stride >= row, f"{name}: tokens must not overlap")
+    if stride < row:
+        raise ValueError(f"{name}: tokens must not overlap")
     return stride
+
+
+def _like(t, x, name) -> None:
+    if not (t.shape == x.shape and t.dtype == x.dtype and t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous, x's shape and dtype")
 
 
 def _sequences(lead, cu_seqlens):
@@ -100,15 +137,11 @@ def _scratch(need: int, workspace, dev):
     return workspace
 
 
-def _raise(status: int, where: str) -> None:
-    if status != 0:
-        raise GdnError(status, where)
-
-
 # -------------------------------------------------------------------- conv ----
 def _conv_args(x, weight, bias, state, lead_dims: int, activation, name):
     _need(activation in GDN_ACT, "activation must be 'silu' or 'none'")
-    _need(x.dim() == lead_dims + 1, f"{name}: x must have {lead_dims + 1} dimensions")
+    if x.dim() != lead_dims + 1:
+        raise ValueError(f"{name}: x must have {lead_dims + 1} dimensions")
     _need(x.dtype in GDN_DTYPE, "x must be bf16 or fp32")
     C = x.shape[-1]
     _need(weight.dim() == 2 and weight.shape[0] == C, "weight must be [C, W]")
@@ -119,8 +152,8 @@ def _conv_args(x, weight, bias, state, lead_dims: int, activation, name):
 
 
 def _conv_state(t, shape, x, name):
-    _need(t is None or (tuple(t.shape) == shape and t.dtype == x.dtype and t.is_contiguous()),
-          f"{name} must be contiguous {list(shape)} in x's dtype")
+    if t is not None and not (t.shape == shape and t.dtype == x.dtype and t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {list(shape)} in x's dtype")
 
 
 def gdn_conv_prefill_into(x, weight, bias, state_in, cu_seqlens, y, state_out,
@@ -134,13 +167,10 @@ def gdn_conv_prefill_into(x, weight, bias, state_in, cu_seqlens, y, state_out,
     _conv_state(state_in, shape, x, "state_in")
     _need(state_out is not None, "state_out is needed")
     _conv_state(state_out, shape, x, "state_out")
-    _need(y.shape == x.shape and y.dtype == x.dtype and y.is_contiguous(),
-          "y must be contiguous, x's shape and dtype")
-    with torch.cuda.device(dev):
-        _raise(lib.gdn_conv_prefill(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state_in),
-                                    _ptr(cu_seqlens), n, T, C, W, GDN_DTYPE[x.dtype],
-                                    GDN_ACT[activation], _ptr(y), _ptr(state_out),
-                                    _stream(stream, dev)), "gdn_conv_prefill")
+    _like(y, x, "y")
+    _call(lib.gdn_conv_prefill, "gdn_conv_prefill", dev, stream, _ptr(x), xs, _ptr(weight),
+          _ptr(bias), _ptr(state_in), _ptr(cu_seqlens), n, T, C, W, GDN_DTYPE[x.dtype],
+          GDN_ACT[activation], _ptr(y), _ptr(state_out))
 
 
 def gdn_conv_prefill(x, weight, bias=None, state_in=None, cu_seqlens=None,
@@ -164,12 +194,10 @@ def gdn_conv_decode_into(x, weight, bias, state, y, activation: str = "silu",
     dev = _device(x, weight, bias, state, y)
     C, W, xs = _conv_args(x, weight, bias, state, 1, activation, "gdn_conv_decode")
     _conv_state(state, (x.shape[0], W - 1, C), x, "state")
-    _need(y.shape == x.shape and y.dtype == x.dtype and y.is_contiguous(),
-          "y must be contiguous, x's shape and dtype")
-    with torch.cuda.device(dev):
-        _raise(lib.gdn_conv_decode(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state),
-                                   x.shape[0], C, W, GDN_DTYPE[x.dtype], GDN_ACT[activation],
-                                   _ptr(y), _stream(stream, dev)), "gdn_conv_decode")
+    _like(y, x, "y")
+    _call(lib.gdn_conv_decode, "gdn_conv_decode", dev, stream, _ptr(x), xs, _ptr(weight),
+          _ptr(bias), _ptr(state), x.shape[0], C, W, GDN_DTYPE[x.dtype], GDN_ACT[activation],
+          _ptr(y))
 
 
 def gdn_conv_decode(x, weight, bias, state, activation: str = "silu", stream=None):
@@ -189,27 +217,25 @@ def gdn_conv_backward(x, weight, dy, bias=None, state_in=None, cu_seqlens=None,
     shape = (n, W - 1, C)
     _conv_state(state_in, shape, x, "state_in")
     _conv_state(dstate_out, shape, x, "dstate_out")
-    _need(dy.shape == x.shape and dy.dtype == x.dtype and dy.is_contiguous(),
-          "dy must be contiguous, x's shape and dtype")
+    _like(dy, x, "dy")
     need = int(lib.gdn_conv_backward_workspace_bytes(n, T, C, W, int(cu_seqlens is not None)))
     ws = _scratch(need, workspace, dev)
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     dw = torch.empty((C, W), dtype=torch.float32, device=dev)
     db = torch.empty((C,), dtype=torch.float32, device=dev)
     ds = torch.empty(shape, dtype=x.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _raise(lib.gdn_conv_backward(
-            _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(cu_seqlens), n, T, C, W,
-            GDN_DTYPE[x.dtype], GDN_ACT[activation], _ptr(dy), _ptr(dstate_out), _ptr(ws),
-            0 if ws is None else ws.numel(), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ds),
-            _stream(stream, dev)), "gdn_conv_backward")
+    _call(lib.gdn_conv_backward, "gdn_conv_backward", dev, stream, _ptr(x), xs, _ptr(weight),
+          _ptr(bias), _ptr(state_in), _ptr(cu_seqlens), n, T, C, W, GDN_DTYPE[x.dtype],
+          GDN_ACT[activation], _ptr(dy), _ptr(dstate_out), _ptr(ws), 0 if ws is None else
+          ws.numel(), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ds))
     return dx, dw, db, ds
 
 
 # -------------------------------------------------------------------- scan ----
 def _scan_args(x, dt, A, B, C, D, dt_bias, lead: int, name):
-    _need(x.dim() == lead + 2 and B.dim() == lead + 2 and C.shape == B.shape
-          and dt.dim() == lead + 1, f"{name}: x [.., H, P], dt [.., H], B and C [.., G, N]")
+    if not (x.dim() == lead + 2 and B.dim() == lead + 2 and C.shape == B.shape
+            and dt.dim() == lead + 1):
+        raise ValueError(f"{name}: x [.., H, P], dt [.., H], B and C [.., G, N]")
     H, P = x.shape[-2:]
     G, N = B.shape[-2:]
     _need(x.shape[:lead] == B.shape[:lead] and dt.shape == x.shape[:-1],
@@ -237,16 +263,13 @@ def gdn_scan_prefill_into(x, dt, A, B, C, D, dt_bias, state_in, cu_seqlens, y, s
     _f32((n, H, N, P), "state_in", state_in)
     _need(state_out is not None, "state_out is needed")
     _f32((n, H, N, P), "state_out", state_out)
-    _need(y.shape == x.shape and y.dtype == x.dtype and y.is_contiguous(),
-          "y must be contiguous, x's shape and dtype")
+    _like(y, x, "y")
     need = int(lib.gdn_scan_prefill_workspace_bytes(n, T, H, P, G, N, GDN_DTYPE[x.dtype],
                                                     int(cu_seqlens is not None)))
     ws = _scratch(need, workspace, dev)
-    with torch.cuda.device(dev):
-        _raise(lib.gdn_scan_prefill(*args, _ptr(state_in), _ptr(cu_seqlens), n, T, H, P, G, N,
-                                    GDN_DTYPE[x.dtype], _ptr(ws), 0 if ws is None else ws.numel(),
-                                    _ptr(y), _ptr(state_out), _stream(stream, dev)),
-               "gdn_scan_prefill")
+    _call(lib.gdn_scan_prefill, "gdn_scan_prefill", dev, stream, *args, _ptr(state_in),
+          _ptr(cu_seqlens), n, T, H, P, G, N, GDN_DTYPE[x.dtype], _ptr(ws), 0 if ws is None else
+          ws.numel(), _ptr(y), _ptr(state_out))
 
 
 def gdn_scan_prefill(x, dt, A, B, C, D=None, dt_bias=None, state_in=None, cu_seqlens=None,
@@ -273,11 +296,9 @@ def gdn_scan_decode_into(x, dt, A, B, C, state, y, D=None, dt_bias=None, stream=
     n = x.shape[0]
     _need(state is not None, "state is needed")
     _f32((n, H, N, P), "state", state)
-    _need(y.shape == x.shape and y.dtype == x.dtype and y.is_contiguous(),
-          "y must be contiguous, x's shape and dtype")
-    with torch.cuda.device(dev):
-        _raise(lib.gdn_scan_decode(*args, _ptr(state), n, H, P, G, N, GDN_DTYPE[x.dtype], _ptr(y),
-                                   _stream(stream, dev)), "gdn_scan_decode")
+    _like(y, x, "y")
+    _call(lib.gdn_scan_decode, "gdn_scan_decode", dev, stream, *args, _ptr(state), n, H, P, G,
+          N, GDN_DTYPE[x.dtype], _ptr(y))
 
 
 def gdn_scan_decode(x, dt, A, B, C, state, D=None, dt_bias=None, stream=None):
@@ -296,8 +317,7 @@ def gdn_scan_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, state_in=None, c
     n, T = _sequences(x.shape[:2], cu_seqlens)
     _f32((n, H, N, P), "state_in", state_in)
     _f32((n, H, N, P), "dstate_out", dstate_out)
-    _need(dy.shape == x.shape and dy.dtype == x.dtype and dy.is_contiguous(),
-          "dy must be contiguous, x's shape and dtype")
+    _like(dy, x, "dy")
     need = int(lib.gdn_scan_backward_workspace_bytes(n, T, H, P, G, N, GDN_DTYPE[x.dtype],
                                                      int(cu_seqlens is not None)))
     ws = _scratch(need, workspace, dev)
@@ -306,12 +326,10 @@ def gdn_scan_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, state_in=None, c
     dB, dC = new(B.shape, x.dtype), new(B.shape, x.dtype)
     dA, dD, db = (new((H,), torch.float32) for _ in range(3))
     ds = new((n, H, N, P), torch.float32)
-    with torch.cuda.device(dev):
-        _raise(lib.gdn_scan_backward(
-            *args, _ptr(state_in), _ptr(cu_seqlens), n, T, H, P, G, N, GDN_DTYPE[x.dtype],
-            _ptr(dy), _ptr(dstate_out), _ptr(ws), 0 if ws is None else ws.numel(), _ptr(dx),
-            _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(db), _ptr(ds),
-            _stream(stream, dev)), "gdn_scan_backward")
+    _call(lib.gdn_scan_backward, "gdn_scan_backward", dev, stream, *args, _ptr(state_in),
+          _ptr(cu_seqlens), n, T, H, P, G, N, GDN_DTYPE[x.dtype], _ptr(dy), _ptr(dstate_out),
+          _ptr(ws), 0 if ws is None else ws.numel(), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB),
+          _ptr(dC), _ptr(dD), _ptr(db), _ptr(ds))
     return dx, ddt, dA, dB, dC, dD, db, ds
 
 
@@ -381,10 +399,9 @@ def gdn_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, qdq: str = 
         y = new(x.shape, torch.int8)
         scales = new(x.shape[:-1] + (d // group,), torch.float32)
     s = None if residual is None else new(x.shape, x.dtype)
-    with torch.cuda.device(dev):
-        _raise(lib.gdn_norm(_ptr(x), xs, _ptr(residual), rs, _ptr(gate), gs, _ptr(weight), tokens,
-                            heads, d, float(eps), GDN_DTYPE[x.dtype], GDN_NORM_OUT[qdq], _ptr(y),
-                            _ptr(scales), _ptr(s), _stream(stream, dev)), "gdn_norm")
+    _call(lib.gdn_norm, "gdn_norm", dev, stream, _ptr(x), xs, _ptr(residual), rs, _ptr(gate),
+          gs, _ptr(weight), tokens, heads, d, float(eps), GDN_DTYPE[x.dtype], GDN_NORM_OUT[qdq],
+          _ptr(y), _ptr(scales), _ptr(s))
     return (y if scales is None else QuantizedRows(y, scales, qdq)), s
 
 
@@ -405,9 +422,8 @@ def gdn_norm_backward(x, weight, dy, gate=None, dresidual=None, eps: float = 1e-
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     dw = torch.empty((d,), dtype=torch.float32, device=dev)
     dg = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _raise(lib.gdn_norm_backward(
-            _ptr(x), xs, _ptr(gate), gs, _ptr(weight), _ptr(dy), ys, _ptr(dresidual), rs, tokens,
-            heads, d, float(eps), GDN_DTYPE[x.dtype], _ptr(ws), 0 if ws is None else ws.numel(),
-            _ptr(dx), _ptr(dw), _ptr(dg), _stream(stream, dev)), "gdn_norm_backward")
+    _call(lib.gdn_norm_backward, "gdn_norm_backward", dev, stream, _ptr(x), xs, _ptr(gate), gs,
+          _ptr(weight), _ptr(dy), ys, _ptr(dresidual), rs, tokens, heads, d, float(eps),
+          GDN_DTYPE[x.dtype], _ptr(ws), 0 if ws is None else ws.numel(), _ptr(dx), _ptr(dw),
+          _ptr(dg))
     return dx, dw, dg

@@ -7,10 +7,13 @@
 // with the state's rows in the places of the tokens before the first one.
 //
 // All three are bound by HBM (two planes of the sequence forward, three
-// backward, 2 W - 1 flops a byte at most).  A thread owns a vector of
-// channels (16 bytes forward) and walks a run of tokens with the last W - 1
-// inputs in registers, so that x is read once but for the W - 1 rows in
-// front of a run; a warp's lanes are neighbouring vectors.
+// backward).  A thread owns four channels (8 bytes of bf16: three CTAs of 256
+// threads fit an SM, where 16-byte vectors leave two and ran 70 us against
+// 65 on 16384 x 4352) and walks a run of tokens with the last W - 1 inputs
+// in registers, so that x is read once but for the W - 1 rows in front of a
+// run; a warp's lanes are neighbouring vectors.
+#include <type_traits>
+
 #include "gdn_layer.cuh"
 #include "gdn_host.cuh"
 #include "gdn_layer.h"
@@ -20,43 +23,95 @@ namespace conv {
 
 using namespace layer;
 
-constexpr int kWarps = 8;  // runs of one CTA, one a warp
+constexpr int kWarps = 8;     // runs of one CTA, one a warp
+constexpr int kWarpsBwd = 2;  // the gradient's: small CTAs, so that a sequence's end idles few warps
 
+// Channels in packed fp32 pairs: V / 2 of them, or one with an idle half.
+template <int V>
+struct Pairs {
+  static constexpr int n = (V + 1) / 2;
+  uint64_t p[n];
+  __device__ __forceinline__ void from(const float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) p[i] = f2_pack(f[2 * i], 2 * i + 1 < V ? f[2 * i + 1 < V ? 2 * i + 1 : 0] : 0.0f);
+  }
+  __device__ __forceinline__ void to(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      float a, b;
+      f2_unpack(p[i], a, b);
+      f[2 * i] = a;
+      if (2 * i + 1 < V) f[2 * i + 1 < V ? 2 * i + 1 : 0] = b;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < n; ++i) p[i] = 0;
+  }
+};
+
+// 1 / (1 + e^-a), 1 / (1 + e^-b).  bf16 results take the approximate base-2
+// exponential and reciprocal (each within 2^-22 or so), fp32 ones the
+// accurate forms; past the exponential's range both give the limits 0 and 1.
 template <typename T>
-__device__ __forceinline__ float act_fwd(float p, bool silu) {
-  return silu ? p * sigmoid<T>(p) : p;
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t x) {
+  float a, b;
+  if constexpr (sizeof(T) == 4) {
+    f2_unpack(x, a, b);
+    return f2_pack(sigmoid<T>(a), sigmoid<T>(b));
+  }
+  f2_unpack(f2_mul(x, f2_pack(-1.44269504f, -1.44269504f)), a, b);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+  f2_unpack(f2_add(f2_pack(a, b), f2_pack(1.0f, 1.0f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return f2_pack(a, b);
 }
-template <typename T>
-__device__ __forceinline__ float act_grad(float p, bool silu) {
-  if (!silu) return 1.0f;
-  const float s = sigmoid<T>(p);
-  return s * (1.0f + p * (1.0f - s));
+template <typename T, bool SILU>
+__device__ __forceinline__ uint64_t act_fwd(uint64_t p) {
+  if constexpr (SILU) return f2_mul(p, sigmoid2<T>(p));
+  return p;
+}
+// s (1 + p (1 - s)) for SiLU
+template <typename T, bool SILU>
+__device__ __forceinline__ uint64_t act_grad(uint64_t p) {
+  const uint64_t one = f2_pack(1.0f, 1.0f);
+  if constexpr (SILU) {
+    const uint64_t s = sigmoid2<T>(p);
+    return f2_mul(s, f2_fma(p, f2_fma(s, f2_pack(-1.0f, -1.0f), one), one));
+  }
+  return one;
 }
 
-// w[v][j] of V channels from c0 on (rows of W, fp32; a row of four taps in
-// one load where the pointer allows it).
+// The taps w[j] and the bias of V channels from c0 on (weight rows of W,
+// fp32; a row of four taps in one load where the pointer allows it).
 template <int V, int W>
-__device__ __forceinline__ void load_taps(const float *w, long long c0, float (&t)[V][W]) {
+__device__ __forceinline__ void load_taps(const float *w, const float *b, long long c0,
+                                          Pairs<V> (&taps)[W], Pairs<V> &bias) {
+  float t[W][V], f[V];
+  bool done = false;
   if constexpr (W == 4) {
     if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float4 r = __ldg(reinterpret_cast<const float4 *>(w + (c0 + v) * 4));
-        t[v][0] = r.x; t[v][1] = r.y; t[v][2] = r.z; t[v][3] = r.w;
+        t[0][v] = r.x; t[1][v] = r.y; t[2][v] = r.z; t[3][v] = r.w;
       }
-      return;
+      done = true;
     }
   }
+  if (!done) {
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < W; ++j) t[v][j] = __ldg(w + (c0 + v) * W + j);
-}
-
-template <int V>
-__device__ __forceinline__ void load_bias(const float *b, long long c0, float (&f)[V]) {
+      for (int j = 0; j < W; ++j) t[j][v] = __ldg(w + (c0 + v) * W + j);
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) f[v] = b ? __ldg(b + c0 + v) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < W; ++j) taps[j].from(t[j]);
+  bias.from(f);
 }
 
 // Row `pos` (0 = first token of the sequence) of V channels; negative
@@ -73,17 +128,19 @@ __device__ __forceinline__ Vec<T, V> row_or_state(const T *x, long long xs, long
 }
 
 // Forward.  grid = (slots, channel blocks); warp w of a CTA takes tokens
-// [RUN w, RUN (w + 1)) of the slot's tile.  RUN rows are loaded U at a time,
-// so a thread keeps U 16-byte loads in flight.  The thread of a sequence's
+// [RUN w, RUN (w + 1)) of the slot's tile.  Products run on packed fp32
+// pairs.  16384 x 4352 bf16: 65 us, 67 % of the copy rate; the special
+// function unit (an exponential and a reciprocal an element) is 58 % busy.
+// The thread of a sequence's
 // first run also writes the new state, after it has read the old one, which
 // may be the same memory.
-template <typename T, int V, int W, int RUN>
-__global__ void __launch_bounds__(32 * kWarps)
+template <typename T, int V, int W, bool SILU, int RUN>
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) * V == 8 ? 3 : 1)
 conv_fwd_kernel(const T *x, long long xs, const float *__restrict__ weight,
                 const float *__restrict__ bias, const T *state_in,
-                const int *__restrict__ cu, int n_seq, int T_, int C, bool silu, T *y,
+                const int *__restrict__ cu, int n_seq, int T_, int C, T *y,
                 T *state_out, unsigned *err) {
-  constexpr int U = RUN < 8 ? RUN : 8;
+  constexpr int U = 8;  // rows a group; the next group's loads are in flight meanwhile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (cu && blockIdx.x == 0 && blockIdx.y == 0) check_seqlens(cu, n_seq, T_, err);
   const Tile t = find_tile(cu, n_seq, T_, RUN * kWarps, blockIdx.x);
@@ -93,11 +150,13 @@ conv_fwd_kernel(const T *x, long long xs, const float *__restrict__ weight,
   const long long p0 = (long long)t.tile * (RUN * kWarps) + warp * RUN;
   if (p0 >= t.len && !(p0 == 0)) return;
 
-  float win[W - 1][V];
+  Pairs<V> hist[W - 1 + U];  // the last W - 1 inputs, then the group's
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k)
-    row_or_state<T, V, W>(x, xs, t.start, p0 - (W - 1) + k, state_in, t.seq, C, c0).get(win[k]);
-
+  for (int k = 0; k < W - 1; ++k) {
+    float f[V];
+    row_or_state<T, V, W>(x, xs, t.start, p0 - (W - 1) + k, state_in, t.seq, C, c0).get(f);
+    hist[k].from(f);
+  }
   if (p0 == 0) {  // the new state: the last W - 1 rows of [old state; x]
     Vec<T, V> last[W - 1];
 #pragma unroll
@@ -108,70 +167,92 @@ conv_fwd_kernel(const T *x, long long xs, const float *__restrict__ weight,
       last[k].store(state_out + ((long long)t.seq * (W - 1) + k) * C + c0);
   }
 
-  float taps[V][W], b[V];
-  load_taps<V, W>(weight, c0, taps);
-  load_bias<V>(bias, c0, b);
-  const long long n = min((long long)RUN, t.len - p0);
+  Pairs<V> taps[W], bias2;
+  load_taps<V, W>(weight, bias, c0, taps, bias2);
+  const int n = (int)max(0LL, min((long long)RUN, t.len - p0));
   const T *xp = x + (t.start + p0) * xs + c0;
   T *yp = y + (t.start + p0) * C + c0;
+  Vec<T, V> next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < n) next[u].load(xp + u * xs);
+#pragma unroll 1
   for (int base = 0; base < n; base += U) {
     Vec<T, V> in[U];
 #pragma unroll
+    for (int u = 0; u < U; ++u) in[u] = next[u];
+    xp += U * xs;
+#pragma unroll
     for (int u = 0; u < U; ++u)
-      if (base + u < n) in[u].load(xp + (base + u) * xs);
+      if (base + U + u < n) next[u].load(xp + u * xs);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (base + u >= n) break;
-      float f[V], o[V];
+      float f[V];
       in[u].get(f);
+      hist[W - 1 + u].from(f);
+      Pairs<V> o;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float p = b[v];
+      for (int i = 0; i < Pairs<V>::n; ++i) {
+        uint64_t p = bias2.p[i];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) p = fmaf(taps[v][j], win[j][v], p);
-        p = fmaf(taps[v][W - 1], f[v], p);
-        o[v] = act_fwd<T>(p, silu);
-#pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
-        win[W - 2][v] = f[v];
+        for (int j = 0; j < W; ++j) p = f2_fma(taps[j].p[i], hist[u + j].p[i], p);
+        o.p[i] = act_fwd<T, SILU>(p);
       }
+      o.to(f);
       Vec<T, V> out;
-      out.set(o);
-      out.store(yp + (long long)(base + u) * C);
+      out.set(f);
+      if (base + u < n) out.store(yp + (long long)u * C);
     }
+    yp += (long long)U * C;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) hist[k] = hist[U + k];
   }
 }
 
-// One token a sequence; the state moves up by one row in place.
-template <typename T, int V, int W>
+// One token a sequence; the state moves up by one row in place.  A thread
+// takes S sequences, so that the taps, 4 W bytes a channel against the
+// 4 W bytes of bf16 state, input and output, are read once for all of them.
+template <typename T, int V, int W, bool SILU, int S>
 __global__ void __launch_bounds__(128)
 conv_decode_kernel(const T *x, long long xs, const float *__restrict__ weight,
-                   const float *__restrict__ bias, T *state, int C, bool silu, T *y) {
-  const long long s = blockIdx.x;
+                   const float *__restrict__ bias, T *state, int n_seq, int C, T *y) {
+  const long long s0 = (long long)blockIdx.x * S;
   const long long c0 = ((long long)blockIdx.y * blockDim.x + threadIdx.x) * V;
   if (c0 >= C) return;
-  Vec<T, V> rows[W];
-  T *st = state + s * (W - 1) * C + c0;
+  Vec<T, V> rows[S][W];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) rows[k].load(st + (long long)k * C);
-  rows[W - 1].load(x + s * xs + c0);
-  float taps[V][W], p[V];
-  load_taps<V, W>(weight, c0, taps);
-  load_bias<V>(bias, c0, p);
+  for (int i = 0; i < S; ++i) {
+    if (s0 + i >= n_seq) break;
+    const T *st = state + (s0 + i) * (W - 1) * C + c0;
 #pragma unroll
-  for (int k = 0; k < W; ++k) {
-    float f[V];
-    rows[k].get(f);
-#pragma unroll
-    for (int v = 0; v < V; ++v) p[v] = fmaf(taps[v][k], f[v], p[v]);
+    for (int k = 0; k < W - 1; ++k) rows[i][k].load(st + (long long)k * C);
+    rows[i][W - 1].load(x + (s0 + i) * xs + c0);
   }
+  Pairs<V> taps[W], b;
+  load_taps<V, W>(weight, bias, c0, taps, b);
 #pragma unroll
-  for (int v = 0; v < V; ++v) p[v] = act_fwd<T>(p[v], silu);
-  Vec<T, V> out;
-  out.set(p);
-  out.store(y + s * C + c0);
+  for (int i = 0; i < S; ++i) {
+    if (s0 + i >= n_seq) break;
+    Pairs<V> p = b;
+    float f[V];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) rows[k + 1].store(st + (long long)k * C);
+    for (int k = 0; k < W; ++k) {
+      Pairs<V> r;
+      rows[i][k].get(f);
+      r.from(f);
+#pragma unroll
+      for (int j = 0; j < Pairs<V>::n; ++j) p.p[j] = f2_fma(taps[k].p[j], r.p[j], p.p[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < Pairs<V>::n; ++j) p.p[j] = act_fwd<T, SILU>(p.p[j]);
+    p.to(f);
+    Vec<T, V> out;
+    out.set(f);
+    out.store(y + (s0 + i) * C + c0);
+    T *st = state + (s0 + i) * (W - 1) * C + c0;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) rows[i][k + 1].store(st + (long long)k * C);
+  }
 }
 
 // Gradient.  A warp walks its run of tokens [p0, p1) and W - 1 tokens more:
@@ -180,118 +261,152 @@ conv_decode_kernel(const T *x, long long xs, const float *__restrict__ weight,
 // and writes the gradient of the state's rows.  The weights' gradients are
 // summed in registers over the run, over the CTA's warps in shared memory,
 // and go to partial[slot] ([W + 1][C], the bias last); conv_reduce_kernel
-// adds the slots in order, so that results do not depend on timing.
-template <typename T, int V, int W, int RUN>
-__global__ void __launch_bounds__(32 * kWarps)
+// adds the slots in order, so that results do not depend on timing.  Groups
+// of rows away from the run's ends skip every test.  16 packed sequences,
+// 13.6 thousand tokens x 2304 bf16: 66 us, 43 % of the copy rate, bound by
+// the latency of 16 warps an SM (128 registers each: the window, dp, taps
+// and five sums); runs of 64 in CTAs of two warps against 73 us with runs
+// of 45 in CTAs of eight.
+template <typename T, int V, int W, bool SILU, int RUN>
+__global__ void __launch_bounds__(32 * kWarpsBwd, sizeof(T) * V == 8 ? 8 : 4)
 conv_bwd_kernel(const T *x, long long xs, const float *__restrict__ weight,
                 const float *__restrict__ bias, const T *__restrict__ state_in,
-                const int *__restrict__ cu, int n_seq, int T_, int C, bool silu,
+                const int *__restrict__ cu, int n_seq, int T_, int C,
                 const T *__restrict__ dy, const T *__restrict__ dstate_out,
                 float *__restrict__ partial, T *__restrict__ dx, T *__restrict__ dstate_in,
                 unsigned *err) {
-  __shared__ float sums[kWarps][W + 1][32 * V];
+  __shared__ float sums[kWarpsBwd][W + 1][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (cu && blockIdx.x == 0 && blockIdx.y == 0) check_seqlens(cu, n_seq, T_, err);
-  const Tile t = find_tile(cu, n_seq, T_, RUN * kWarps, blockIdx.x);
+  const Tile t = find_tile(cu, n_seq, T_, RUN * kWarpsBwd, blockIdx.x);
   const long long c0 = ((long long)blockIdx.y * 32 + lane) * V;
-  const long long p0 = (long long)t.tile * (RUN * kWarps) + warp * RUN;
-  float dw[V][W], db[V];
+  const long long p0 = (long long)t.tile * (RUN * kWarpsBwd) + warp * RUN;
+  Pairs<V> dw[W], db;
+  db.zero();
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    db[v] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) dw[v][j] = 0.0f;
-  }
+  for (int j = 0; j < W; ++j) dw[j].zero();
   if (t.seq >= 0 && c0 < C && (p0 < t.len || p0 == 0)) {
-    const long long p1 = min(p0 + RUN, t.len);
-    float taps[V][W], b[V], xw[W - 1][V], dpw[W - 1][V];
-    load_taps<V, W>(weight, c0, taps);
-    load_bias<V>(bias, c0, b);
+    constexpr int U = 4;
+    const int n = (int)max(0LL, min((long long)RUN, t.len - p0));     // own rows
+    const int all = (int)min((long long)n + W - 1, t.len - p0);       // and those behind them
+    Pairs<V> taps[W], bias2, xh[W - 1 + U], dh[W - 1 + U];
+    load_taps<V, W>(weight, bias, c0, taps, bias2);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-      row_or_state<T, V, W>(x, xs, t.start, p0 - (W - 1) + k, state_in, t.seq, C, c0).get(xw[k]);
-#pragma unroll
-      for (int v = 0; v < V; ++v) dpw[k][v] = 0.0f;
+      float f[V];
+      row_or_state<T, V, W>(x, xs, t.start, p0 - (W - 1) + k, state_in, t.seq, C, c0).get(f);
+      xh[k].from(f);
+      dh[k].zero();
     }
-    const long long first = p0 == 0 ? -(W - 1) : p0;  // first row written
-    // Rows p0 .. p1 - 1 + (W - 1); past the sequence's end dp is zero.
-    constexpr int U = 4;
-    for (long long base = p0; base < p1 + (W - 1); base += U) {
+    const int first = p0 == 0 ? -(W - 1) : 0;                         // first row written
+    const int kept = (int)max(-(long long)W, min(t.len - (W - 1) - p0, 0x7fffffffLL));  // in the new state from here
+    const T *xp = x + (t.start + p0) * xs + c0, *gp = dy + (t.start + p0) * C + c0;
+    Vec<T, V> xn[U], gn[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      xn[u].zero();
+      gn[u].zero();
+      if (u < all) {
+        xn[u].load(xp + u * xs);
+        gn[u].load(gp + (long long)u * C);
+      }
+    }
+    // One group of U rows.  INSIDE: every row is one of the run's own, writes
+    // a row of dx, and neither it nor what it writes is in a state.
+    auto group = [&](int base, auto inside) {
+      constexpr bool INSIDE = decltype(inside)::value;
       Vec<T, V> xin[U], gin[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool in = base + u < t.len && base + u < p1 + (W - 1);
-        if (in) {
-          xin[u].load(x + (t.start + base + u) * xs + c0);
-          gin[u].load(dy + (t.start + base + u) * C + c0);
-        } else {
-          xin[u].zero();
-          gin[u].zero();
+        xin[u] = xn[u];
+        gin[u] = gn[u];
+      }
+      xp += U * xs;
+      gp += (long long)U * C;
+      if (base + 2 * U <= all) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          xn[u].load(xp + u * xs);
+          gn[u].load(gp + (long long)u * C);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          xn[u].zero();
+          gn[u].zero();
+          if (base + U + u < all) {
+            xn[u].load(xp + u * xs);
+            gn[u].load(gp + (long long)u * C);
+          }
         }
       }
+      T *op = dx + (t.start + p0 + base - (W - 1)) * C + c0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const long long pos = base + u;
-        if (pos >= p1 + (W - 1)) break;
-        const bool in = pos < t.len;
-        float f[V], g[V], dp[V];
+        const int pos = base + u;
+        float f[V];
+        Pairs<V> g, o;
         xin[u].get(f);
-        gin[u].get(g);
+        xh[W - 1 + u].from(f);
+        gin[u].get(f);
+        g.from(f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float p = b[v];
+        for (int i = 0; i < Pairs<V>::n; ++i) {
+          uint64_t p = bias2.p[i];
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) p = fmaf(taps[v][j], xw[j][v], p);
-          p = fmaf(taps[v][W - 1], f[v], p);
-          dp[v] = in ? g[v] * act_grad<T>(p, silu) : 0.0f;
-          if (pos < p1) {
+          for (int j = 0; j < W; ++j) p = f2_fma(taps[j].p[i], xh[u + j].p[i], p);
+          uint64_t d = f2_mul(g.p[i], act_grad<T, SILU>(p));
+          // rows past the sequence's end: g is zero, but the slope there is
+          // of inputs that may not be finite
+          if (!INSIDE && pos >= all) d = 0;
+          dh[W - 1 + u].p[i] = d;
+          if (INSIDE || pos < n) {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) dw[v][j] = fmaf(dp[v], xw[j][v], dw[v][j]);
-            dw[v][W - 1] = fmaf(dp[v], f[v], dw[v][W - 1]);
-            db[v] += dp[v];
+            for (int j = 0; j < W; ++j) dw[j].p[i] = f2_fma(d, xh[u + j].p[i], dw[j].p[i]);
+            db.p[i] = f2_add(db.p[i], d);
           }
+          // row pos - (W - 1) has all its terms: w_j meets dp_{pos - j}
+          uint64_t s = f2_mul(taps[0].p[i], d);
 #pragma unroll
-          for (int j = 0; j + 1 < W - 1; ++j) xw[j][v] = xw[j + 1][v];
-          xw[W - 2][v] = f[v];
+          for (int j = 1; j < W; ++j) s = f2_fma(taps[j].p[i], dh[W - 1 + u - j].p[i], s);
+          o.p[i] = s;
         }
-        const long long u0 = pos - (W - 1);  // dx_{u0} has all its terms now
-        if (u0 >= first) {
-          float o[V];
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            // w_j meets dp_{u0 + W - 1 - j}: j = 0 the newest
-            float s = taps[v][0] * dp[v];
-#pragma unroll
-            for (int j = 1; j < W; ++j) s = fmaf(taps[v][j], dpw[W - 1 - j][v], s);
-            o[v] = s;
-          }
-          if (dstate_out && u0 >= t.len - (W - 1)) {  // this row is in the new state
+        const int u0 = pos - (W - 1);
+        if (INSIDE || (u0 >= first && u0 < n)) {
+          o.to(f);
+          if (!INSIDE && dstate_out && u0 >= kept) {  // this row is in the new state
             Vec<T, V> e;
-            e.load(dstate_out + ((long long)t.seq * (W - 1) + (u0 - (t.len - (W - 1)))) * C + c0);
+            e.load(dstate_out + ((long long)t.seq * (W - 1) + (p0 + u0 - (t.len - (W - 1)))) * C + c0);
             float f2[V];
             e.get(f2);
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] += f2[v];
+            for (int v = 0; v < V; ++v) f[v] += f2[v];
           }
           Vec<T, V> out;
-          out.set(o);
-          if (u0 >= 0) out.store(dx + (t.start + u0) * C + c0);
+          out.set(f);
+          if (INSIDE || u0 >= 0) out.store(op + (long long)u * C);
           else out.store(dstate_in + ((long long)t.seq * (W - 1) + (W - 1 + u0)) * C + c0);
         }
-#pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-          for (int v = 0; v < V; ++v) dpw[j][v] = dpw[j + 1][v];
-#pragma unroll
-        for (int v = 0; v < V; ++v) dpw[W - 2][v] = dp[v];
       }
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) {
+        xh[k] = xh[U + k];
+        dh[k] = dh[U + k];
+      }
+    };
+    const int calm = dstate_out ? min(n, kept + W - 1) : n;  // groups that end here are inside
+#pragma unroll 1
+    for (int base = 0; base < n + W - 1; base += U) {
+      if (base >= W - 1 && base + U <= calm) group(base, std::true_type{});
+      else group(base, std::false_type{});
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
+  for (int j = 0; j <= W; ++j) {
+    float f[V];
+    (j < W ? dw[j < W ? j : 0] : db).to(f);
 #pragma unroll
-    for (int j = 0; j < W; ++j) sums[warp][j][lane * V + v] = dw[v][j];
-    sums[warp][W][lane * V + v] = db[v];
+    for (int v = 0; v < V; ++v) sums[warp][j][lane * V + v] = f[v];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += blockDim.x) {
@@ -300,7 +415,7 @@ conv_bwd_kernel(const T *x, long long xs, const float *__restrict__ weight,
     if (ch >= C) continue;
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += sums[w][j][c];
+    for (int w = 0; w < kWarpsBwd; ++w) s += sums[w][j][c];
     partial[((long long)blockIdx.x * (W + 1) + j) * C + ch] = s;
   }
 }
@@ -330,7 +445,7 @@ conv_reduce_kernel(const float *__restrict__ partial, long long slots, int C, in
 }
 
 // ------------------------------------------------------------------ host ----
-constexpr int kRun = 32, kRunShort = 8, kRunBwd = 32;
+constexpr int kRun = 32, kRunShort = 8, kRunBwd = 64;
 
 struct Args {
   const void *x;
@@ -351,36 +466,42 @@ gdn_status check(const Args &a, gdn_dtype dt, int act) {
 
 bool vector_ok(const void *p, size_t bytes) { return !p || aligned_to(p, bytes); }
 
-template <typename T, int V, int W, int RUN>
+template <typename T, int V, int W, bool SILU, int RUN>
 gdn_status fwd_launch(const Args &a, void *y, void *so, unsigned *err, cudaStream_t st) {
   const long long slots = slot_count(a.n_seq, a.T, RUN * kWarps, a.cu != nullptr);
   const long long cb = (a.C + 32LL * V - 1) / (32 * V);
   if (slots > 0x7fffffffLL || cb > 65535) return GDN_ERR_UNSUPPORTED;
-  conv_fwd_kernel<T, V, W, RUN><<<dim3((unsigned)slots, (unsigned)cb), 32 * kWarps, 0, st>>>(
+  conv_fwd_kernel<T, V, W, SILU, RUN><<<dim3((unsigned)slots, (unsigned)cb), 32 * kWarps, 0, st>>>(
       static_cast<const T *>(a.x), a.xs, a.w, a.b, static_cast<const T *>(a.state_in), a.cu,
-      a.n_seq, a.T, a.C, a.silu, static_cast<T *>(y), static_cast<T *>(so), err);
+      a.n_seq, a.T, a.C, static_cast<T *>(y), static_cast<T *>(so), err);
   return launched();
 }
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool SILU>
 gdn_status fwd_run(const Args &a, void *y, void *so, unsigned *err, cudaStream_t st) {
   // Runs of 32 tokens re-read 3 rows in 32; a call too small to give every
   // SM two such CTAs takes runs of 8, which spreads it over four times as many.
   const long long cb = (a.C + 32LL * V - 1) / (32 * V);
   if (slot_count(a.n_seq, a.T, kRun * kWarps, a.cu != nullptr) * cb < 2 * 148)
-    return fwd_launch<T, V, W, kRunShort>(a, y, so, err, st);
-  return fwd_launch<T, V, W, kRun>(a, y, so, err, st);
+    return fwd_launch<T, V, W, SILU, kRunShort>(a, y, so, err, st);
+  return fwd_launch<T, V, W, SILU, kRun>(a, y, so, err, st);
 }
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool SILU>
 gdn_status decode_run(const Args &a, void *state, void *y, cudaStream_t st) {
   const long long nv = (a.C + V - 1) / V;
   const int threads = nv >= 128 ? 128 : (int)((nv + 31) / 32 * 32);
   const long long cb = (nv + threads - 1) / threads;
   if (cb > 65535) return GDN_ERR_UNSUPPORTED;
-  conv_decode_kernel<T, V, W><<<dim3((unsigned)a.n_seq, (unsigned)cb), threads, 0, st>>>(
-      static_cast<const T *>(a.x), a.xs, a.w, a.b, static_cast<T *>(state), a.C, a.silu,
-      static_cast<T *>(y));
+  // four sequences a thread where that still leaves every SM a CTA
+  if (a.n_seq * cb >= 4 * 148)
+    conv_decode_kernel<T, V, W, SILU, 4><<<dim3((unsigned)((a.n_seq + 3LL) / 4), (unsigned)cb), threads, 0, st>>>(
+        static_cast<const T *>(a.x), a.xs, a.w, a.b, static_cast<T *>(state), a.n_seq, a.C,
+        static_cast<T *>(y));
+  else
+    conv_decode_kernel<T, V, W, SILU, 1><<<dim3((unsigned)a.n_seq, (unsigned)cb), threads, 0, st>>>(
+        static_cast<const T *>(a.x), a.xs, a.w, a.b, static_cast<T *>(state), a.n_seq, a.C,
+        static_cast<T *>(y));
   return launched();
 }
 
@@ -392,14 +513,14 @@ struct BwdArgs {
   void *dsi;
 };
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool SILU>
 gdn_status bwd_run(const Args &a, const BwdArgs &g, unsigned *err, cudaStream_t st) {
-  const long long slots = slot_count(a.n_seq, a.T, kRunBwd * kWarps, a.cu != nullptr);
+  const long long slots = slot_count(a.n_seq, a.T, kRunBwd * kWarpsBwd, a.cu != nullptr);
   const long long cb = (a.C + 32LL * V - 1) / (32 * V);
   if (slots > 0x7fffffffLL || cb > 65535) return GDN_ERR_UNSUPPORTED;
-  conv_bwd_kernel<T, V, W, kRunBwd><<<dim3((unsigned)slots, (unsigned)cb), 32 * kWarps, 0, st>>>(
+  conv_bwd_kernel<T, V, W, SILU, kRunBwd><<<dim3((unsigned)slots, (unsigned)cb), 32 * kWarpsBwd, 0, st>>>(
       static_cast<const T *>(a.x), a.xs, a.w, a.b, static_cast<const T *>(a.state_in), a.cu,
-      a.n_seq, a.T, a.C, a.silu, static_cast<const T *>(g.dy), static_cast<const T *>(g.dso),
+      a.n_seq, a.T, a.C, static_cast<const T *>(g.dy), static_cast<const T *>(g.dso),
       g.partial, static_cast<T *>(g.dx), static_cast<T *>(g.dsi), err);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   conv_reduce_kernel<<<dim3((unsigned)((a.C + 31) / 32), (unsigned)(W + 1)), 32 * kWarps, 0, st>>>(
@@ -407,9 +528,12 @@ gdn_status bwd_run(const Args &a, const BwdArgs &g, unsigned *err, cudaStream_t 
   return launched();
 }
 
-#define GDN_CONV_W(FN, T, V, ...)                         \
-  (a.W == 4 ? FN<T, V, 4>(__VA_ARGS__)                    \
-            : a.W == 3 ? FN<T, V, 3>(__VA_ARGS__) : FN<T, V, 2>(__VA_ARGS__))
+#define GDN_CONV_A(FN, T, V, W, ...) \
+  (a.silu ? FN<T, V, W, true>(__VA_ARGS__) : FN<T, V, W, false>(__VA_ARGS__))
+#define GDN_CONV_W(FN, T, V, ...)                      \
+  (a.W == 4   ? GDN_CONV_A(FN, T, V, 4, __VA_ARGS__)   \
+   : a.W == 3 ? GDN_CONV_A(FN, T, V, 3, __VA_ARGS__)   \
+              : GDN_CONV_A(FN, T, V, 2, __VA_ARGS__))
 
 // Vectors need aligned pointers and a channel count and token stride that
 // keep every row aligned; other calls go element by element.
@@ -449,8 +573,8 @@ gdn_status gdn_conv_prefill(const void *x, int64_t x_stride, const float *weight
       return GDN_CONV_W(conv::fwd_run, float, 4, a, y, state_out, err, st);
     return GDN_CONV_W(conv::fwd_run, float, 1, a, y, state_out, err, st);
   }
-  if (conv::vec(a, e, 8, {x, y, state_in, state_out}))
-    return GDN_CONV_W(conv::fwd_run, __nv_bfloat16, 8, a, y, state_out, err, st);
+  if (conv::vec(a, e, 4, {x, y, state_in, state_out}))
+    return GDN_CONV_W(conv::fwd_run, __nv_bfloat16, 4, a, y, state_out, err, st);
   return GDN_CONV_W(conv::fwd_run, __nv_bfloat16, 1, a, y, state_out, err, st);
 }
 
@@ -479,7 +603,7 @@ gdn_status gdn_conv_decode(const void *x, int64_t x_stride, const float *weight,
 
 size_t gdn_conv_backward_workspace_bytes(int n_seq, int T, int C, int W, int packed) {
   if (n_seq <= 0 || T < 0 || C <= 0 || W < 2 || W > 4) return 0;
-  return (size_t)layer::slot_count(n_seq, T, conv::kRunBwd * conv::kWarps, packed != 0) *
+  return (size_t)layer::slot_count(n_seq, T, conv::kRunBwd * conv::kWarpsBwd, packed != 0) *
          (size_t)(W + 1) * C * sizeof(float);
 }
 

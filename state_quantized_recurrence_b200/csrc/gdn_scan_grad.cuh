@@ -98,7 +98,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
   fetch_tile<N, 256>(sC, in.C + row0 * in.cs + grp * N, in.cs, n, tid);
   if (h0 < h1) {
     fetch_head(h0);
-    if (warp == 0) decays_of(in, row0, n, h0, in.A[h0], in.bias ? in.bias[h0] : 0.0f, dec[0]);
+    if (warp == 0) decays_of(raw_steps(in, row0, n, h0), n, in.A[h0], in.bias ? in.bias[h0] : 0.0f, dec[0]);
   }
   copy_commit();
 
@@ -417,7 +417,8 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       fetch_head(h + 1);
       copy_commit();
       if (warp == 7)
-        decays_of(in, row0, n, h + 1, in.A[h + 1], in.bias ? in.bias[h + 1] : 0.0f, dec[(h + 1 - h0) & 1]);
+        decays_of(raw_steps(in, row0, n, h + 1), n, in.A[h + 1], in.bias ? in.bias[h + 1] : 0.0f,
+                  dec[(h + 1 - h0) & 1]);
     }
     // l_t, four threads a token
     {

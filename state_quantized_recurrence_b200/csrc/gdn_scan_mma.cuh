@@ -33,7 +33,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
 }
 // d[16 x 8] += a[16 x 16] b[16 x 8]
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -119,9 +119,20 @@ __device__ __forceinline__ float exp2_of(double v) {
   asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(h));
   return r * fmaf(l, 0.693147181f, 1.0f);
 }
-// By one warp, two tokens a lane; tokens past n have step 0 and decay 1.
-__device__ __forceinline__ void decays_of(const In<__nv_bfloat16> &in, long long row0, int n, int h,
-                                          float A, float bias, Decays &m) {
+// The raw steps of a chunk, two tokens a lane, loaded well before they are used.
+struct RawSteps {
+  __nv_bfloat16 v[2];
+};
+__device__ __forceinline__ RawSteps raw_steps(const In<__nv_bfloat16> &in, long long row0, int n, int h) {
+  const int t = 2 * (threadIdx.x & 31);
+  RawSteps r;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    r.v[k] = t + k < n ? in.raw[(row0 + t + k) * in.rs + h] : __nv_bfloat16(0.0f);
+  return r;
+}
+// By one warp; tokens past n have step 0 and decay 1.
+__device__ __forceinline__ void decays_of(const RawSteps &raw, int n, float A, float bias, Decays &m) {
   const int lane = threadIdx.x & 31;
   double a[2];
   float dt[2];
@@ -131,7 +142,7 @@ __device__ __forceinline__ void decays_of(const In<__nv_bfloat16> &in, long long
     dt[k] = 0.0f;
     float sg = 0.0f;
     if (t < n) {
-      const float v = to_f32(in.raw[(row0 + t) * in.rs + h]) + bias;
+      const float v = to_f32(raw.v[k]) + bias;
       dt[k] = softplus(v);
       sg = 1.0f / (1.0f + expf(-v));
     }
@@ -256,7 +267,7 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
     fetch_tile<N, 128>(sB, Bp + row_of(c) * Bs, Bs, rows_in(c), tid);
     fetch_tile<64, 128>(sX, Xp + row_of(c) * Xs, Xs, rows_in(c), tid);
     copy_commit();
-    if (warp == 0) decays_of(in, row_of(c), rows_in(c), h, A, bias, dec[0]);
+    if (warp == 0) decays_of(raw_steps(in, row_of(c), rows_in(c), h), rows_in(c), A, bias, dec[0]);
   }
   const float Dh = LEAVE == kY && in.D ? in.D[h] : 0.0f;
 
@@ -264,6 +275,10 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
   for (int k = 0; k < total; ++k) {
     const int c = chunk_at(k);
     const Decays &m = dec[k & 1];
+    const bool more = k + 1 < total;
+    const int cn = more ? chunk_at(k + 1) : c;  // the next chunk
+    RawSteps raw;
+    if (warp == 0 && more) raw = raw_steps(in, row_of(cn), rows_in(cn), h);
     copy_wait<0>();
     __syncthreads();
 
@@ -326,6 +341,8 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(at1), "r"(hi) : "memory");
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(at1 + 8192), "r"(lo) : "memory");
       }
+      // the first warp has the fewest columns of S: it forms the next chunk's decays
+      if (warp == 0 && more) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
       // C S_0, the state's pieces straight from the accumulators
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -341,16 +358,18 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             split2(st[2 * kk + u][2 * e], st[2 * kk + u][2 * e + 1], hb[e][u], lb[e][u]);
+        // eight products between two of one accumulator
+        uint32_t a[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a[4];
-          ldsm4(block_rows<N>(sC, 16 * i, 2 * kk, lane), a);
+        for (int i = 0; i < 4; ++i) ldsm4(block_rows<N>(sC, 16 * i, 2 * kk, lane), a[i]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mma16816(yv[i][e], a, hb[e][0], hb[e][1]);
-            mma16816(yv[i][e], a, lb[e][0], lb[e][1]);
-          }
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma16816(yv[i][e], a[i], hb[e][0], hb[e][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma16816(yv[i][e], a[i], lb[e][0], lb[e][1]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -364,8 +383,7 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
         }
       }
       __syncthreads();  // M is there, C is free
-      if (k + 1 < total) {
-        const int cn = chunk_at(k + 1);
+      if (more) {
         fetch_tile<N, 128>(sC, in.C + grp * N + row_of(cn) * in.cs, in.cs, rows_in(cn), tid);
         copy_commit();
       }
@@ -383,16 +401,15 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
       ldsm4t(tile_at<64>(sX, 16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)), x);
       if constexpr (LEAVE == kY) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i < j) continue;  // above the diagonal
-          uint32_t a[4];
-          ldsm4(block_rows<64>(sM, 16 * i, 2 * j, lane), a);
-          mma16816(yv[i][0], a, x[0], x[2]);
-          mma16816(yv[i][1], a, x[1], x[3]);
-          ldsm4(block_rows<64>(sM + 8192, 16 * i, 2 * j, lane), a);
-          mma16816(yv[i][0], a, x[0], x[2]);
-          mma16816(yv[i][1], a, x[1], x[3]);
-        }
+        for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i < j) continue;  // above the diagonal
+            uint32_t a[4];
+            ldsm4(block_rows<64>(sM + piece * 8192, 16 * i, 2 * j, lane), a);
+            mma16816(yv[i][0], a, x[0], x[2]);
+            mma16816(yv[i][1], a, x[1], x[3]);
+          }
       }
       const float *wv = REV ? m.gam : m.w;
       const float2 wa = *reinterpret_cast<const float2 *>(wv + 16 * j + 2 * q);
@@ -406,15 +423,25 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
         split3(lo * w.x, hi * w.y, u0[e], u1[e], u2[e]);
       }
 #pragma unroll
-      for (int i = 0; i < N / 16; ++i) {
-        uint32_t b[4];
-        ldsm4t(block_rows<N>(sB, 16 * j, 2 * i, lane), b);  // (j, j + 8) x (n, n + 8)
-        mma16816(st[2 * i], u0, b[0], b[1]);
-        mma16816(st[2 * i + 1], u0, b[2], b[3]);
-        mma16816(st[2 * i], u1, b[0], b[1]);
-        mma16816(st[2 * i + 1], u1, b[2], b[3]);
-        mma16816(st[2 * i], u2, b[0], b[1]);
-        mma16816(st[2 * i + 1], u2, b[2], b[3]);
+      for (int i = 0; i < N / 16; i += 2) {
+        uint32_t b[2][4];  // (j, j + 8) x (n, n + 8)
+        ldsm4t(block_rows<N>(sB, 16 * j, 2 * i, lane), b[0]);
+        ldsm4t(block_rows<N>(sB, 16 * j, 2 * i + 2, lane), b[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mma16816(st[2 * (i + e)], u0, b[e][0], b[e][1]);
+          mma16816(st[2 * (i + e) + 1], u0, b[e][2], b[e][3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mma16816(st[2 * (i + e)], u1, b[e][0], b[e][1]);
+          mma16816(st[2 * (i + e) + 1], u1, b[e][2], b[e][3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mma16816(st[2 * (i + e)], u2, b[e][0], b[e][1]);
+          mma16816(st[2 * (i + e) + 1], u2, b[e][2], b[e][3]);
+        }
       }
     }
     if (LEAVE == kEnds) run_decay *= all;
@@ -437,9 +464,8 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
                   bf2_set(fmaf(Dh, xa, yv[i][j][2 * e]), fmaf(Dh, xb, yv[i][j][2 * e + 1]));
           }
     }
-    if (k + 1 < total) {
-      const int cn = chunk_at(k + 1);
-      if (warp == ((k + 1) & 3)) decays_of(in, row_of(cn), rows_in(cn), h, A, bias, dec[(k + 1) & 1]);
+    if (more) {
+      if (LEAVE != kY && warp == 0) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
       __syncthreads();  // B, x and M are free
       fetch_tile<N, 128>(sB, Bp + row_of(cn) * Bs, Bs, rows_in(cn), tid);
       fetch_tile<64, 128>(sX, Xp + row_of(cn) * Xs, Xs, rows_in(cn), tid);
