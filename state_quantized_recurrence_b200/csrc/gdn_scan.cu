@@ -54,22 +54,21 @@ unsigned units(const Call &c) { return (unsigned)(c.n_seq * c.H * (c.P / 64)); }
 
 // Sequences are cut into runs of chunks where (sequence, head, 64 columns)
 // units alone would leave SMs idle: a first launch forms what each run adds
-// to a zero state, and each run of the second starts from those before it.
-// The first launch costs half of the second's time a chunk; three CTAs are
-// resident on an SM.  `waves`: how often over the runs fill the 148 SMs; a
-// forward call gains from two (4 x 4096 tokens x 16 heads of 128: 341 us
-// against 371 with one and 376 with three), the gradient, whose runs also
-// write every chunk's state, from one.
+// to a zero state, a second turns that into the state each run starts from.
+// As many runs as two CTAs on every SM: 4 x 4096 tokens x 16 heads of 128
+// take 326 us so, 345 with half as many and 336 with twice; runs of four
+// chunks at least.
 struct Plan {
   int seg_chunks;   // chunks of a run
   bool split;
   long long slots;  // run slots of the call
-  size_t state, decay, copy, bytes;  // workspace parts
+  size_t state, decay, bytes;  // workspace parts
 };
-constexpr int kResident = 3 * 148;
-Plan plan(int n_seq, int T, int H, int P, int N, bool packed, int waves) {
+constexpr int kResident = 2 * 148;
+// `sweeps`: how many such launches share the device (the gradient's two).
+Plan plan(int n_seq, int T, int H, int P, int N, bool packed, int sweeps) {
   Plan p = {};
-  const long long target = (long long)waves * kResident;
+  const long long target = kResident / sweeps;
   const long long units = (long long)n_seq * H * (P / 64);
   const long long chunks = (T + 63LL) / 64;
   const long long mean = packed && n_seq > 0 ? (chunks + n_seq - 1) / n_seq : chunks;
@@ -87,43 +86,48 @@ Plan plan(int n_seq, int T, int H, int P, int N, bool packed, int waves) {
   p.slots = layer::slot_count(n_seq, T, (int)(seg * 64), packed);
   if (p.split) {
     p.decay = (size_t)p.slots * H * N * P * 4;
-    p.copy = p.decay + ((size_t)p.slots * H * 4 + 15) / 16 * 16;
-    p.bytes = p.copy + (size_t)n_seq * H * N * P * 4;
+    p.bytes = p.decay + ((size_t)p.slots * H * 4 + 15) / 16 * 16;
   }
   return p;
 }
 
-template <int N, int LEAVE, bool REV>
-gdn_status sweep(const In<__nv_bfloat16> &in, const Plan &p, const __nv_bfloat16 *dy,
-                 const float *first, Ends ends, __nv_bfloat16 *y, float *out_state,
-                 uint32_t *chunk_states, unsigned *err, cudaStream_t st) {
-  auto kern = sweep_mma_kernel<N, LEAVE, REV>;
-  constexpr int smem = (int)SweepSmem<N>::bytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return GDN_ERR_CUDA;
-  kern<<<(unsigned)(p.slots * in.H * (in.P / 64)), 128, smem, st>>>(in, dy, first, p.seg_chunks, ends, y,
-                                                                    out_state, chunk_states, err);
+template <typename K>
+bool fits(K kern, int smem) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+}
+unsigned run_blocks(const Call &c, const Plan &p) { return (unsigned)(p.slots * c.H * (c.P / 64)); }
+
+// What the runs add, then what they start from; rev.state: backwards too.
+template <int N>
+gdn_status run_starts(const Call &c, const Plan &p, const __nv_bfloat16 *dy, const float *dstate_out, Ends fwd,
+                      Ends rev, unsigned *err, cudaStream_t st) {
+  const In<__nv_bfloat16> in = typed<__nv_bfloat16>(c);
+  constexpr int smem = (int)SweepSmem<N, kEnds>::bytes;
+  const unsigned both = rev.state ? 2 : 1;
+  if (!fits(ends_mma_kernel<N>, smem)) return GDN_ERR_CUDA;
+  ends_mma_kernel<N><<<dim3(run_blocks(c, p), both), kSweepThreads, smem, st>>>(in, dy, p.seg_chunks, fwd, rev, err);
+  if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+  const long long np = (long long)c.N * c.P;
+  start_states_kernel<<<dim3((unsigned)(c.n_seq * c.H * (np / 1024)), both), 256, 0, st>>>(
+      c.cu, c.n_seq, c.T, c.H, np, c.state_in, dstate_out, p.seg_chunks, fwd, rev);
   return launched();
 }
 
 template <int N>
 gdn_status prefill_mma(const Call &c, char *ws, void *y, float *state_out, unsigned *err, cudaStream_t st) {
-  In<__nv_bfloat16> in = typed<__nv_bfloat16>(c);
-  const Plan p = plan(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr, 2);
-  Ends ends{reinterpret_cast<float *>(ws + p.state), reinterpret_cast<float *>(ws + p.decay)};
+  const In<__nv_bfloat16> in = typed<__nv_bfloat16>(c);
+  const Plan p = plan(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr, 1);
+  Ends ends{nullptr, nullptr};
   if (p.split) {
-    if (in.state_in && in.state_in == state_out) {  // a late run would write what an early one reads
-      float *copy = reinterpret_cast<float *>(ws + p.copy);
-      if (cudaMemcpyAsync(copy, in.state_in, (size_t)c.n_seq * c.H * c.N * c.P * 4,
-                          cudaMemcpyDeviceToDevice, st) != cudaSuccess)
-        return GDN_ERR_CUDA;
-      in.state_in = copy;
-    }
-    const gdn_status s = sweep<N, kEnds, false>(in, p, nullptr, nullptr, ends, nullptr, nullptr, nullptr, err, st);
+    ends = Ends{reinterpret_cast<float *>(ws + p.state), reinterpret_cast<float *>(ws + p.decay)};
+    const gdn_status s = run_starts<N>(c, p, nullptr, nullptr, ends, Ends{nullptr, nullptr}, err, st);
     if (s != GDN_OK) return s;
   }
-  return sweep<N, kY, false>(in, p, nullptr, in.state_in, ends, static_cast<__nv_bfloat16 *>(y), state_out,
-                             nullptr, err, st);
+  constexpr int smem = (int)SweepSmem<N, kY>::bytes;
+  if (!fits(scan_mma_kernel<N>, smem)) return GDN_ERR_CUDA;
+  scan_mma_kernel<N><<<run_blocks(c, p), kSweepThreads, smem, st>>>(
+      in, p.seg_chunks, ends, static_cast<__nv_bfloat16 *>(y), state_out, err);
+  return launched();
 }
 
 gdn_status prefill(const Call &c, gdn_dtype dt, char *ws, void *y, float *state_out, unsigned *err,
@@ -192,13 +196,13 @@ Workspace workspace(int n_seq, int T, int H, int P, int G, int N, gdn_dtype dt, 
   w.part = w.dC + sums;
   w.bytes = w.part + (size_t)w.slots * H * 16;
   if (mma) {
-    w.runs = plan(n_seq, T, H, P, N, packed, 1);
+    w.runs = plan(n_seq, T, H, P, N, packed, 2);
     if (w.runs.split) {
       w.fwd = w.bytes;
       w.fwd_decay = w.fwd + w.runs.decay;
-      w.rev = w.fwd + w.runs.copy;
+      w.rev = w.fwd + w.runs.bytes;
       w.rev_decay = w.rev + w.runs.decay;
-      w.bytes = w.rev + w.runs.copy;
+      w.bytes = w.rev + w.runs.bytes;
     }
   }
   return w;
@@ -254,26 +258,27 @@ gdn_status backward_mma(const Call &c, const Grads &g, char *ws, unsigned *err, 
   const In<T> in = typed<T>(c);
   const Workspace w = workspace(c.n_seq, c.T, c.H, c.P, c.G, c.N, GDN_DTYPE_BF16, c.cu != nullptr);
   const T *dy = static_cast<const T *>(g.dy);
-  const Ends fwd{reinterpret_cast<float *>(ws + w.fwd), reinterpret_cast<float *>(ws + w.fwd_decay)};
-  const Ends rev{reinterpret_cast<float *>(ws + w.rev), reinterpret_cast<float *>(ws + w.rev_decay)};
+  Ends fwd{nullptr, nullptr}, rev{nullptr, nullptr};
   uint32_t *states = reinterpret_cast<uint32_t *>(ws + w.states);
   uint32_t *adjoints = reinterpret_cast<uint32_t *>(ws + w.adjoints);
   gdn_status s;
   if (w.runs.split) {
-    if ((s = sweep<N, kEnds, false>(in, w.runs, nullptr, nullptr, fwd, nullptr, nullptr, nullptr, err, st)) != GDN_OK ||
-        (s = sweep<N, kEnds, true>(in, w.runs, dy, nullptr, rev, nullptr, nullptr, nullptr, err, st)) != GDN_OK)
-      return s;
+    fwd = Ends{reinterpret_cast<float *>(ws + w.fwd), reinterpret_cast<float *>(ws + w.fwd_decay)};
+    rev = Ends{reinterpret_cast<float *>(ws + w.rev), reinterpret_cast<float *>(ws + w.rev_decay)};
+    if ((s = run_starts<N>(c, w.runs, dy, g.dstate_out, fwd, rev, err, st)) != GDN_OK) return s;
   }
-  if ((s = sweep<N, kChunks, false>(in, w.runs, nullptr, c.state_in, fwd, nullptr, nullptr, states, err, st)) != GDN_OK ||
-      (s = sweep<N, kChunks, true>(in, w.runs, dy, g.dstate_out, rev, nullptr, g.dstate_in, adjoints, err, st)) != GDN_OK)
-    return s;
+  constexpr int sweep_smem = (int)SweepSmem<N, kChunks>::bytes;
+  if (!fits(boundaries_mma_kernel<N>, sweep_smem)) return GDN_ERR_CUDA;
+  boundaries_mma_kernel<N><<<dim3(run_blocks(c, w.runs), 2), kSweepThreads, sweep_smem, st>>>(
+      in, dy, g.dstate_out, w.runs.seg_chunks, fwd, rev, states, adjoints, g.dstate_in, err);
+  if ((s = launched()) != GDN_OK) return s;
   auto kern = chunk_grad_mma_kernel<N, P>;
   constexpr int smem = (int)GradSmem<N, P>::bytes;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GDN_ERR_CUDA;
   const GroupOut out{static_cast<T *>(g.dB), static_cast<T *>(g.dC), reinterpret_cast<float *>(ws + w.dB),
                      reinterpret_cast<float *>(ws + w.dC)};
-  kern<<<(unsigned)(w.slots * c.G * w.splits), 256, smem, st>>>(
+  kern<<<(unsigned)(w.slots * c.G * w.splits), kGradThreads, smem, st>>>(
       in, dy, reinterpret_cast<T *>(states), reinterpret_cast<T *>(adjoints), w.splits,
       static_cast<T *>(g.dx), static_cast<T *>(g.draw), out, reinterpret_cast<float *>(ws + w.part));
   if ((s = launched()) != GDN_OK) return s;
@@ -300,7 +305,7 @@ size_t gdn_scan_prefill_workspace_bytes(int n_seq, int T, int H, int P, int G, i
   const scan::Call c{nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, nullptr, nullptr, nullptr,
                      nullptr, nullptr, 0, T, H, P, G, N};
   if (n_seq <= 0 || dtype != GDN_DTYPE_BF16 || scan::check(c, dtype, false) != GDN_OK) return 0;
-  return scan::plan(n_seq, T, H, P, N, packed != 0, 2).bytes;
+  return scan::plan(n_seq, T, H, P, N, packed != 0, 1).bytes;
 }
 
 gdn_status gdn_scan_prefill(const void *x, int64_t x_stride, const void *dt_raw,

@@ -2,7 +2,7 @@
 // algebra of chunk_grad_kernel with mma.sync products of bf16 pieces (pairs
 // for M, W, the states and the adjoints: 2^-17 relative).
 //
-// A CTA of eight warps takes one chunk and a range of one group's heads.
+// A CTA of sixteen warps takes one chunk and a range of one group's heads.
 // S = C B^T is formed once; dB and dC are summed over the heads in the
 // accumulators, so that neither leaves the SM before it is whole (with the
 // heads split over several CTAs, their fp32 parts are added afterwards in
@@ -17,18 +17,18 @@ namespace scan {
 
 template <int N, int P>
 struct GradSmem {
-  static constexpr uint32_t C = 0, B = C + 64 * N * 2;
-  static constexpr uint32_t X = B + 64 * N * 2;            // P / 64 tiles of 64 x 64
-  static constexpr uint32_t Y = X + 64 * P * 2;
-  static constexpr uint32_t H = Y + 64 * P * 2;            // hi, lo: [64 p][N]
-  static constexpr uint32_t G = H + 2 * 64 * N * 2;
-  static constexpr uint32_t M = G + 2 * 64 * N * 2;        // hi, lo
-  static constexpr uint32_t W = M + 2 * 64 * 64 * 2;
-  static constexpr uint32_t Z = W + 2 * 64 * 64 * 2;       // fp32 [64][65]
+  static constexpr uint32_t C = 0, B = C + kTileBytes<N>;
+  static constexpr uint32_t X = B + kTileBytes<N>;         // P / 64 tiles of 64 x 64
+  static constexpr uint32_t Y = X + P / 64 * kTileBytes<64>;
+  static constexpr uint32_t H = Y + P / 64 * kTileBytes<64>;  // hi, lo: [64 p][N]
+  static constexpr uint32_t G = H + 2 * kTileBytes<N>;
+  static constexpr uint32_t M = G + 2 * kTileBytes<N>;     // hi, lo
+  static constexpr uint32_t W = M + 2 * kTileBytes<64>;
+  static constexpr uint32_t Z = W + 2 * kTileBytes<64>;    // fp32 [64][65]
   static constexpr uint32_t V = (Z + 64 * 65 * 4 + 15) / 16 * 16;
   // row sums by warp column: r, q, x . du (4 each), Z block sums [4][64], l, gh and dD by warp
   struct Rows {
-    float r[4][64], q[4][64], xdu[4][64], zb[4][64], l[64], gh[8], dD[8];
+    float r[4][64], q[4][64], xdu[4][64], zb[4][64], l[64], gh[16], dD[16];
   };
   static constexpr uint32_t D = V + (sizeof(Rows) + 15) / 16 * 16;
   static constexpr uint32_t bytes = D + 2 * sizeof(Decays);
@@ -45,8 +45,10 @@ struct GroupOut {
   float *pb, *pc;
 };
 
+constexpr int kGradThreads = 512;
+
 template <int N, int P>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(kGradThreads, 1)
 chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ dy,
                       const __nv_bfloat16 *__restrict__ states,
                       const __nv_bfloat16 *__restrict__ adjoints, int splits,
@@ -70,7 +72,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
   const Tile t = find_tile(in.cu, in.n_seq, in.T_, 64, slot);
   const int n = t.seq < 0 ? 0 : (int)min(64LL, t.len - (long long)t.tile * 64);
   if (n <= 0) {
-    for (int h = h0 + tid; h < h1; h += 256)
+    for (int h = h0 + tid; h < h1; h += kGradThreads)
 #pragma unroll
       for (int k = 0; k < 3; ++k) part[(slot * in.H + h) * 4 + k] = 0.0f;
     return;
@@ -81,43 +83,41 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
   auto fetch_states = [&](int h, int pt) {
     const __nv_bfloat16 *s = states + (slot * in.H + h) * 2 * np + (long long)pt * 64 * N;
     const __nv_bfloat16 *a = adjoints + (slot * in.H + h) * 2 * np + (long long)pt * 64 * N;
-    fetch_tile<N, 256>(sH, s, N, 64, tid);
-    fetch_tile<N, 256>(sH + 64 * N * 2, s + np, N, 64, tid);
-    fetch_tile<N, 256>(sG, a, N, 64, tid);
-    fetch_tile<N, 256>(sG + 64 * N * 2, a + np, N, 64, tid);
+    fetch_tile<N, kGradThreads>(sH, s, N, 64, tid);
+    fetch_tile<N, kGradThreads>(sH + kTileBytes<N>, s + np, N, 64, tid);
+    fetch_tile<N, kGradThreads>(sG, a, N, 64, tid);
+    fetch_tile<N, kGradThreads>(sG + kTileBytes<N>, a + np, N, 64, tid);
   };
   auto fetch_head = [&](int h) {
 #pragma unroll
     for (int pt = 0; pt < kPT; ++pt) {
-      fetch_tile<64, 256>(sX + pt * 8192, in.x + row0 * in.xs + (long long)h * P + pt * 64, in.xs, n, tid);
-      fetch_tile<64, 256>(sY + pt * 8192, dy + (row0 * in.H + h) * P + pt * 64, (long long)in.H * P, n, tid);
+      fetch_tile<64, kGradThreads>(sX + pt * kTileBytes<64>, in.x + row0 * in.xs + (long long)h * P + pt * 64, in.xs, n, tid);
+      fetch_tile<64, kGradThreads>(sY + pt * kTileBytes<64>, dy + (row0 * in.H + h) * P + pt * 64, (long long)in.H * P, n, tid);
     }
     fetch_states(h, 0);
   };
-  fetch_tile<N, 256>(sB, in.B + row0 * in.bs + grp * N, in.bs, n, tid);
-  fetch_tile<N, 256>(sC, in.C + row0 * in.cs + grp * N, in.cs, n, tid);
+  fetch_tile<N, kGradThreads>(sB, in.B + row0 * in.bs + grp * N, in.bs, n, tid);
+  fetch_tile<N, kGradThreads>(sC, in.C + row0 * in.cs + grp * N, in.cs, n, tid);
   if (h0 < h1) {
     fetch_head(h0);
     if (warp == 0) decays_of(raw_steps(in, row0, n, h0), n, in.A[h0], in.bias ? in.bias[h0] : 0.0f, dec[0]);
   }
   copy_commit();
 
-  // S for this warp's 16 rows and 32 columns, unless all lie above the diagonal
-  const int sr = 16 * (warp >> 1), sc = 32 * (warp & 1);
-  const bool lower = sc <= sr + 15;
-  const int gr = 32 * (warp >> 2), gc = (N / 4) * (warp & 3);  // rows, columns of dB and dC
+  // S for this warp's 16 rows and 16 columns, unless all lie above the diagonal
+  const int sr = 16 * (warp >> 2), sc = 16 * (warp & 3);
+  const bool lower = sc <= sr;
+  const int gr = 16 * (warp >> 2), gc = (N / 4) * (warp & 3);  // rows, columns of dB and dC
   const int ur = gr, uc = 16 * (warp & 3);                     // of du
-  float S[4][4], aB[2][2 * kJ][4], aC[2][2 * kJ][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) S[i][e] = 0.0f;
+  float S[2][4], aB[1][2 * kJ][4], aC[1][2 * kJ][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2 * kJ; ++j)
+    for (int e = 0; e < 4; ++e) S[i][e] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) aB[i][j][e] = aC[i][j][e] = 0.0f;
+  for (int j = 0; j < 2 * kJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) aB[0][j][e] = aC[0][j][e] = 0.0f;
 
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
@@ -129,40 +129,34 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       for (int kk = 0; kk < N / 16; ++kk) {
         uint32_t a[4], b[4];
         ldsm4(block_rows<N>(sC, sr, 2 * kk, lane), a);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          ldsm4(block_cols<N>(sB, sc + 16 * j, 2 * kk, lane), b);
-          mma16816(S[2 * j], a, b[0], b[1]);
-          mma16816(S[2 * j + 1], a, b[2], b[3]);
-        }
+        ldsm4(block_cols<N>(sB, sc, 2 * kk, lane), b);
+        mma16816(S[0], a, b[0], b[1]);
+        mma16816(S[1], a, b[2], b[3]);
       }
     }
     // K = dy x^T, then M, W and Z
     float dD = 0.0f;
     if (lower) {
-      float K[4][4];
+      float K[2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) K[i][e] = 0.0f;
 #pragma unroll
       for (int kk = 0; kk < P / 16; ++kk) {
-        const uint32_t tx = sX + (kk / 4) * 8192, ty = sY + (kk / 4) * 8192;
+        const uint32_t tx = sX + (kk / 4) * kTileBytes<64>, ty = sY + (kk / 4) * kTileBytes<64>;
         uint32_t a[4], b[4];
         ldsm4(block_rows<64>(ty, sr, 2 * (kk % 4), lane), a);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          ldsm4(block_cols<64>(tx, sc + 16 * j, 2 * (kk % 4), lane), b);
-          mma16816(K[2 * j], a, b[0], b[1]);
-          mma16816(K[2 * j + 1], a, b[2], b[3]);
-        }
+        ldsm4(block_cols<64>(tx, sc, 2 * (kk % 4), lane), b);
+        mma16816(K[0], a, b[0], b[1]);
+        mma16816(K[1], a, b[2], b[3]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = sr + g + 8 * e;
         const float hr = m.hi[r], lr = m.lo[r];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
           const int c = sc + 8 * j + 2 * q;
           float mv[2], wv[2];
 #pragma unroll
@@ -175,17 +169,17 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
             sZ[r * 65 + c + u] = s * wv[u];
           }
           uint32_t hi, lo;
-          const uint32_t at = (uint32_t)r * 128 + ((uint32_t)((c >> 3) ^ (r & 7)) << 4) + q * 4;
+          const uint32_t at = tile_at<64>(0, r, c / 8) + q * 4;
           split2(mv[0], mv[1], hi, lo);
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(sM + at), "r"(hi) : "memory");
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sM + 8192 + at), "r"(lo) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sM + kTileBytes<64> + at), "r"(lo) : "memory");
           split2(wv[0], wv[1], hi, lo);
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + at), "r"(hi) : "memory");
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + 8192 + at), "r"(lo) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + kTileBytes<64> + at), "r"(lo) : "memory");
         }
       }
     } else {  // above the diagonal: Z alone is read there
-      for (int i = lane; i < 16 * 32; i += 32) sZ[(sr + i / 32) * 65 + sc + i % 32] = 0.0f;
+      for (int i = lane; i < 16 * 16; i += 32) sZ[(sr + i / 16) * 65 + sc + i % 16] = 0.0f;
     }
     dD = warp_sum(dD);
     if (lane == 0) rs.dD[warp] = dD;
@@ -193,7 +187,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
     __syncthreads();
 
     // Z summed from each 16-row block's last row up
-    {
+    if (tid < 256) {
       const int c = tid & 63, b = tid >> 6;
       float s = 0.0f;
 #pragma unroll
@@ -207,17 +201,16 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       uint32_t b[kJ][4];
-      const bool need_c = kk <= gr / 16 + 1, need_b = kk >= gr / 16;
+      const bool need_c = kk <= gr / 16, need_b = kk >= gr / 16;
       if (need_c) {
 #pragma unroll
         for (int j = 0; j < kJ; ++j) ldsm4t(block_rows<N>(sB, 16 * kk, gc / 8 + 2 * j, lane), b[j]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (kk > gr / 16 + i) continue;
+        for (int i = 0; i < 1; ++i) {
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece) {
             uint32_t a[4];
-            ldsm4(block_rows<64>(sW + piece * 8192, gr + 16 * i, 2 * kk, lane), a);
+            ldsm4(block_rows<64>(sW + piece * kTileBytes<64>, gr + 16 * i, 2 * kk, lane), a);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
               mma16816(aC[i][2 * j], a, b[j][0], b[j][1]);
@@ -230,12 +223,11 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
 #pragma unroll
         for (int j = 0; j < kJ; ++j) ldsm4t(block_rows<N>(sC, 16 * kk, gc / 8 + 2 * j, lane), b[j]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (kk < gr / 16 + i) continue;
+        for (int i = 0; i < 1; ++i) {
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece) {
             uint32_t a[4];
-            ldsm4t(block_cols<64>(sW + piece * 8192, 16 * kk, (gr + 16 * i) / 8, lane), a);
+            ldsm4t(block_cols<64>(sW + piece * kTileBytes<64>, 16 * kk, (gr + 16 * i) / 8, lane), a);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
               mma16816(aB[i][2 * j], a, b[j][0], b[j][1]);
@@ -245,12 +237,11 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
         }
       }
     }
-    float rsum[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, qsum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    float xsum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    float rsum[1][2] = {{0.f, 0.f}}, qsum[1][2] = {{0.f, 0.f}}, xsum[1][2] = {{0.f, 0.f}};
     const float Dh = in.D ? in.D[h] : 0.0f;
 #pragma unroll 1
     for (int pt = 0; pt < kPT; ++pt) {
-      const uint32_t tX = sX + pt * 8192, tY = sY + pt * 8192;
+      const uint32_t tX = sX + pt * kTileBytes<64>, tY = sY + pt * kTileBytes<64>;
       if (pt > 0) {
         __syncthreads();  // the first tile's states have been read
         fetch_states(h, pt);
@@ -262,33 +253,33 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         const uint32_t tA = side ? tX : tY, tS = side ? sG : sH, tO = side ? sB : sC;
-        float T[2][2 * kJ][4];
+        float T[1][2 * kJ][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 1; ++i)
 #pragma unroll
           for (int j = 0; j < 2 * kJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) T[i][j][e] = 0.0f;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          uint32_t a[2][4];
+          uint32_t a[1][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) ldsm4(block_rows<64>(tA, gr + 16 * i, 2 * kk, lane), a[i]);
+          for (int i = 0; i < 1; ++i) ldsm4(block_rows<64>(tA, gr + 16 * i, 2 * kk, lane), a[i]);
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
               uint32_t b[4];
-              ldsm4t(block_rows<N>(tS + piece * 64 * N * 2, 16 * kk, gc / 8 + 2 * j, lane), b);
+              ldsm4t(block_rows<N>(tS + piece * kTileBytes<N>, 16 * kk, gc / 8 + 2 * j, lane), b);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
+              for (int i = 0; i < 1; ++i) {
                 mma16816(T[i][2 * j], a[i], b[0], b[1]);
                 mma16816(T[i][2 * j + 1], a[i], b[2], b[3]);
               }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 1; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = gr + 16 * i + g + 8 * e;
@@ -316,25 +307,24 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       }
       // du = M^T dy + e^{c_n - c_j} B G^T, dx, x . du
       {
-        float U[2][2][4], T[2][2][4];
+        float U[1][2][4], T[1][2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 1; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) U[i][j][e] = T[i][j][e] = 0.0f;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          if (kk < ur / 16) continue;
+          if (kk < ur / 16) continue;  // above the diagonal
           uint32_t b[4];
           ldsm4t(block_rows<64>(tY, 16 * kk, uc / 8, lane), b);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (kk < ur / 16 + i) continue;
+          for (int i = 0; i < 1; ++i) {
 #pragma unroll
             for (int piece = 0; piece < 2; ++piece) {
               uint32_t a[4];
-              ldsm4t(block_cols<64>(sM + piece * 8192, 16 * kk, (ur + 16 * i) / 8, lane), a);
+              ldsm4t(block_cols<64>(sM + piece * kTileBytes<64>, 16 * kk, (ur + 16 * i) / 8, lane), a);
               mma16816(U[i][0], a, b[0], b[1]);
               mma16816(U[i][1], a, b[2], b[3]);
             }
@@ -342,22 +332,22 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
         }
 #pragma unroll
         for (int kk = 0; kk < N / 16; ++kk) {
-          uint32_t a[2][4];
+          uint32_t a[1][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) ldsm4(block_rows<N>(sB, ur + 16 * i, 2 * kk, lane), a[i]);
+          for (int i = 0; i < 1; ++i) ldsm4(block_rows<N>(sB, ur + 16 * i, 2 * kk, lane), a[i]);
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece) {
             uint32_t b[4];
-            ldsm4(block_cols<N>(sG + piece * 64 * N * 2, uc, 2 * kk, lane), b);
+            ldsm4(block_cols<N>(sG + piece * kTileBytes<N>, uc, 2 * kk, lane), b);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 1; ++i) {
               mma16816(T[i][0], a[i], b[0], b[1]);
               mma16816(T[i][1], a[i], b[2], b[3]);
             }
           }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 1; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = ur + 16 * i + g + 8 * e;
@@ -380,13 +370,13 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
           }
       }
       // <G, H0>
-      for (int i = tid; i < 64 * N / 8; i += 256) {
-        const uint32_t at = (uint32_t)i * 16;
+      for (int i = tid; i < 64 * N / 8; i += kGradThreads) {
+        const uint32_t at = tile_at<N>(0, i / (N / 8), i % (N / 8));
         uint32_t a[4], b[4], c[4], d[4];
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(sH + at));
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]) : "r"(sH + 64 * N * 2 + at));
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]) : "r"(sH + kTileBytes<N> + at));
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(sG + at));
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(sG + 64 * N * 2 + at));
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(sG + kTileBytes<N> + at));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float p0, p1, l0, l1, g0, g1, k0, k1;
@@ -399,7 +389,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 1; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = gr + 16 * i + g + 8 * e;
@@ -416,12 +406,12 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
     if (h + 1 < h1) {
       fetch_head(h + 1);
       copy_commit();
-      if (warp == 7)
+      if (warp == 15)
         decays_of(raw_steps(in, row0, n, h + 1), n, in.A[h + 1], in.bias ? in.bias[h + 1] : 0.0f,
                   dec[(h + 1 - h0) & 1]);
     }
     // l_t, four threads a token
-    {
+    if (tid < 256) {
       const int tt = tid >> 2, b = tid & 3;
       float s = 0.0f;
       for (int c = 16 * b; c < min(16 * b + 16, tt); ++c) {
@@ -435,7 +425,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       if (b == 0) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) v += rs.gh[w];
+        for (int w = 0; w < 16; ++w) v += rs.gh[w];
         rs.l[tt] = fmaf(m.all, v, s);
       }
     }
@@ -460,7 +450,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
         float *po = part + (slot * in.H + h) * 4;
         float d = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) d += rs.dD[w];
+        for (int w = 0; w < 16; ++w) d += rs.dD[w];
         po[0] = dA;
         po[1] = d;
         po[2] = db;
@@ -468,7 +458,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
     }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 1; ++i)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = gr + 16 * i + g + 8 * e;

@@ -16,6 +16,7 @@
 #pragma once
 
 #include "gdn_scan_simt.cuh"
+#include "gdn_sm100.cuh"
 
 namespace gdn {
 namespace scan {
@@ -52,29 +53,41 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // (a, b) as bf16 pairs: hi + lo (+ lo2), each the rounding of what is left.
+__device__ __forceinline__ void rest_of(float &a, float &b, uint32_t piece) {
+  float p, q;
+  bf2_get(piece, p, q);
+  f2_unpack(f2_fma(f2_pack(p, q), f2_pack(-1.0f, -1.0f), f2_pack(a, b)), a, b);
+}
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
   hi = bf2_set(a, b);
-  float ha, hb;
-  bf2_get(hi, ha, hb);
-  lo = bf2_set(a - ha, b - hb);
+  rest_of(a, b, hi);
+  lo = bf2_set(a, b);
 }
 __device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-  float p, q;
   hi = bf2_set(a, b);
-  bf2_get(hi, p, q);
-  a -= p;
-  b -= q;
+  rest_of(a, b, hi);
   mid = bf2_set(a, b);
-  bf2_get(mid, p, q);
-  lo = bf2_set(a - p, b - q);
+  rest_of(a, b, mid);
+  lo = bf2_set(a, b);
+}
+// v *= s
+__device__ __forceinline__ void scale4(float (&v)[4], float s) {
+  const uint64_t k = f2_pack(s, s);
+  f2_unpack(f2_mul(f2_pack(v[0], v[1]), k), v[0], v[1]);
+  f2_unpack(f2_mul(f2_pack(v[2], v[3]), k), v[2], v[3]);
 }
 
-// Address of 16-byte column `ch` of row r in a tile with rows of COLS bf16:
-// the low three bits of the column are exchanged with the row's, so that
-// eight rows of one column lie in different banks.
+// Tiles of 64 rows of COLS bf16 with 16 bytes behind each row: eight rows of
+// one 16-byte column lie in different banks, and an address is a lane's own
+// part plus a constant (exchanging column bits with the row's instead costs
+// three instructions a load, a tenth of all that the sweeps execute).
+template <int COLS>
+constexpr uint32_t kRowBytes = COLS * 2 + 16;
+template <int COLS>
+constexpr uint32_t kTileBytes = 64 * kRowBytes<COLS>;
 template <int COLS>
 __device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int ch) {
-  return tile + (uint32_t)r * (COLS * 2) + ((uint32_t)(ch ^ (r & 7)) << 4);
+  return tile + (uint32_t)r * kRowBytes<COLS> + (uint32_t)ch * 16;
 }
 // The four 8 x 8 blocks of a 16 x 16 block at (r0, column ch0), rows first
 // (an A operand as it lies, or with .trans a transposed one's columns) ...
@@ -182,37 +195,106 @@ enum Leave : int {
   kChunks = 2  // the state at every chunk's start (backwards: end), as bf16 pairs
 };
 
-template <int N>
+template <int N, int LEAVE>
 struct SweepSmem {
-  static constexpr uint32_t C = 0, B = C + 64 * N * 2, X = B + 64 * N * 2, M = X + 64 * 64 * 2;
-  static constexpr uint32_t D = M + 2 * 64 * 64 * 2;
+  static constexpr bool Y = LEAVE == kY;
+  static constexpr uint32_t C = 0, B = C + (Y ? kTileBytes<N> : 0), X = B + 2 * kTileBytes<N>;
+  static constexpr uint32_t M = X + 2 * kTileBytes<64>;
+  static constexpr uint32_t E = M + (Y ? 2 * kTileBytes<64> : 0);    // halves of C S_0 on their way
+  static constexpr uint32_t O = E + (Y ? 8 * 16 * 32 * 4 : 0);    // a chunk's state on its way out
+  static constexpr uint32_t D = O + (LEAVE == kChunks ? 2 * kTileBytes<N> : 0);
   static constexpr uint32_t bytes = D + 2 * sizeof(Decays);
 };
+constexpr int kSweepThreads = 256;
 
-struct Ends {           // kEnds writes, the others read
-  float *state;         // [segment slot][H][N][P]
-  float *decay;         // [segment slot][H]
+struct Ends {           // of the runs, where sequences are cut into several
+  float *state;         // [run slot][H][N][P]; NULL: one run a sequence
+  float *decay;         // [run slot][H]
 };
+
+// From what each run adds to zero (kEnds) to the state that each run starts
+// from, in place: run k starts from decay_{k-1} start_{k-1} + added_{k-1}.
+// A thread follows four state elements through the runs of a sequence.
+// Bound by latency; it keeps every run from adding up all that went before
+// it.
+template <bool REV>
+__device__ __forceinline__ void start_states(const int *__restrict__ cu, int n_seq, int T, int H, long long np,
+                                             const float *__restrict__ first, int seg_chunks, Ends ends) {
+  const int parts = (int)(np / 1024);
+  const int part = blockIdx.x % parts, h = blockIdx.x / parts % H;
+  const long long s = blockIdx.x / parts / H;
+  const long long L = seg_chunks * 64LL;
+  long long len = T, slot;
+  if (cu) {
+    if (!seq_ok(cu, n_seq, (int)s, T)) return;
+    len = cu[s + 1] - cu[s];
+    slot = s + cu[s] / L;
+  } else {
+    slot = s * (T > 0 ? (T + L - 1) / L : 1);
+  }
+  const int segs = (int)max(1LL, (len + L - 1) / L);
+  const long long at = part * 1024 + threadIdx.x * 4;
+  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (first) run = *reinterpret_cast<const float4 *>(first + (s * H + h) * np + at);
+  constexpr int kAhead = 8;  // runs loaded before the first is needed
+  for (int k0 = 0; k0 < segs; k0 += kAhead) {
+    float4 add[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u;
+      if (k >= segs - 1) continue;  // the last run adds to nobody
+      const long long w = slot + (REV ? segs - 1 - k : k);
+      add[u] = *reinterpret_cast<const float4 *>(ends.state + (w * H + h) * np + at);
+      d[u] = ends.decay[w * H + h];
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u;
+      if (k >= segs) break;
+      const long long w = slot + (REV ? segs - 1 - k : k);
+      *reinterpret_cast<float4 *>(ends.state + (w * H + h) * np + at) = run;
+      if (k == segs - 1) break;
+      run.x = fmaf(d[u], run.x, add[u].x);
+      run.y = fmaf(d[u], run.y, add[u].y);
+      run.z = fmaf(d[u], run.z, add[u].z);
+      run.w = fmaf(d[u], run.w, add[u].w);
+    }
+  }
+}
+// blockIdx.y = 1 (where there are two): the adjoints, from the last run on.
+__global__ void __launch_bounds__(256)
+start_states_kernel(const int *__restrict__ cu, int n_seq, int T, int H, long long np, const float *first,
+                    const float *last, int seg_chunks, Ends fwd, Ends rev) {
+  if (blockIdx.y == 0) start_states<false>(cu, n_seq, T, H, np, first, seg_chunks, fwd);
+  else start_states<true>(cu, n_seq, T, H, np, last, seg_chunks, rev);
+}
 
 // REV: the adjoint G backwards over the chunks, G_0 = e^{c_n} G_n + sum_i
 // e^{c_i} C_i dy_i^T, with C in B's place, dy in x's and e^{c_i} in w's.
 template <int N, int LEAVE, bool REV>
-__global__ void __launch_bounds__(128, 3)
-sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ dy,
-                 const float *first_state, int seg_chunks, Ends ends, __nv_bfloat16 *__restrict__ y,
-                 float *out_state, uint32_t *__restrict__ chunk_states, unsigned *err) {
-  using S = SweepSmem<N>;
+__device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __nv_bfloat16 *__restrict__ dy,
+                                          const float *first_state, int seg_chunks, Ends ends,
+                                          __nv_bfloat16 *__restrict__ y, float *out_state,
+                                          uint32_t *__restrict__ chunk_states, unsigned *err) {
+  using S = SweepSmem<N, LEAVE>;
+  constexpr int kT = N / 16;  // tiles of 8 columns in a warp's half of N
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t sC = smem_at(smem) + S::C, sB = smem_at(smem) + S::B, sX = smem_at(smem) + S::X;
+  const uint32_t sC = smem_at(smem) + S::C, sB0 = smem_at(smem) + S::B, sX0 = smem_at(smem) + S::X;
   const uint32_t sM = smem_at(smem) + S::M;
   Decays *dec = reinterpret_cast<Decays *>(smem + S::D);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pw = warp & 3, nh = warp >> 2;  // 16 columns of P, half of N
   const int g = lane >> 2, q = lane & 3;
   const int npt = in.P / 64;
   const int pt = blockIdx.x % npt, h = blockIdx.x / npt % in.H;
-  const long long slot = blockIdx.x / npt / in.H;
+  long long slot = blockIdx.x / npt / in.H;
   const int grp = h / (in.H / in.G);
   if (in.cu && blockIdx.x == 0) check_seqlens(in.cu, in.n_seq, in.T_, err);
+  // Packed sequences that are not cut into runs (one slot each, and one past
+  // the last) go longest first: the short ones fill the tail.
+  if (in.cu && seg_chunks * 64LL >= in.T_ && in.n_seq <= kSweepThreads && slot < in.n_seq)
+    slot = seq_of_rank(in.cu, in.n_seq, (int)slot);
   const Tile t = find_tile(in.cu, in.n_seq, in.T_, seg_chunks * 64, slot);
   if (t.seq < 0) return;
   const long long row_end = t.start + t.len;
@@ -223,32 +305,22 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
   if (LEAVE == kEnds && last_seg) return;                  // nobody follows
   const float A = in.A[h], bias = in.bias ? in.bias[h] : 0.0f;
 
-  // the state's (p, n) of this thread: rows 16 warp + g (+ 8) of P, columns
-  // 8 i + 2 q (+ 1) of N
-  float st[N / 8][4];
-  const long long p0 = pt * 64 + warp * 16 + g;
+  // the state's (p, n) of this thread: rows 16 pw + g (+ 8) of P, columns
+  // nh N / 2 + 8 i + 2 q (+ 1) of N
+  float st[kT][4];
+  const long long p0 = pt * 64 + pw * 16 + g;
+  const int n0 = nh * (N / 2) + 2 * q;
   const long long np = (long long)N * in.P;
+  auto at = [&](int i, int e) { return (n0 + 8 * i + (e & 1)) * (long long)in.P + (e >> 1) * 8; };
   {
-    const float *src = LEAVE == kEnds || !first_state ? nullptr
-                       : first_state + ((long long)t.seq * in.H + h) * np + p0;
+    const float *src = LEAVE == kEnds ? nullptr
+                       : ends.state   ? ends.state + (slot * in.H + h) * np + p0
+                       : first_state  ? first_state + ((long long)t.seq * in.H + h) * np + p0
+                                      : nullptr;
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i)
+    for (int i = 0; i < kT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        st[i][e] = src ? src[(8 * i + 2 * q + (e & 1)) * (long long)in.P + (e >> 1) * 8] : 0.0f;
-  }
-  if (LEAVE != kEnds) {  // what the runs before this one add
-    const int before = REV ? segs - 1 - t.tile : t.tile;
-    for (int k = 0; k < before; ++k) {
-      const long long s = slot + (REV ? before - k : k - before);
-      const float d = ends.decay[s * in.H + h];
-      const float *src = ends.state + (s * in.H + h) * np + p0;
-#pragma unroll
-      for (int i = 0; i < N / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          st[i][e] = fmaf(d, st[i][e], src[(8 * i + 2 * q + (e & 1)) * (long long)in.P + (e >> 1) * 8]);
-    }
+      for (int e = 0; e < 4; ++e) st[i][e] = src ? src[at(i, e)] : 0.0f;
   }
 
   const __nv_bfloat16 *Bp = REV ? in.C + grp * N : in.B + grp * N;
@@ -263,11 +335,12 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
 
   if (total > 0) {
     const int c = chunk_at(0);
-    if (LEAVE == kY) fetch_tile<N, 128>(sC, in.C + grp * N + row_of(c) * in.cs, in.cs, rows_in(c), tid);
-    fetch_tile<N, 128>(sB, Bp + row_of(c) * Bs, Bs, rows_in(c), tid);
-    fetch_tile<64, 128>(sX, Xp + row_of(c) * Xs, Xs, rows_in(c), tid);
+    if (LEAVE == kY)
+      fetch_tile<N, kSweepThreads>(sC, in.C + grp * N + row_of(c) * in.cs, in.cs, rows_in(c), tid);
+    fetch_tile<N, kSweepThreads>(sB0, Bp + row_of(c) * Bs, Bs, rows_in(c), tid);
+    fetch_tile<64, kSweepThreads>(sX0, Xp + row_of(c) * Xs, Xs, rows_in(c), tid);
     copy_commit();
-    if (warp == 0) decays_of(raw_steps(in, row_of(c), rows_in(c), h), rows_in(c), A, bias, dec[0]);
+    if (warp == 7) decays_of(raw_steps(in, row_of(c), rows_in(c), h), rows_in(c), A, bias, dec[0]);
   }
   const float Dh = LEAVE == kY && in.D ? in.D[h] : 0.0f;
 
@@ -275,75 +348,98 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
   for (int k = 0; k < total; ++k) {
     const int c = chunk_at(k);
     const Decays &m = dec[k & 1];
+    const uint32_t sB = sB0 + (k & 1) * kTileBytes<N>, sX = sX0 + (k & 1) * kTileBytes<64>;
     const bool more = k + 1 < total;
     const int cn = more ? chunk_at(k + 1) : c;  // the next chunk
     RawSteps raw;
-    if (warp == 0 && more) raw = raw_steps(in, row_of(cn), rows_in(cn), h);
+    if (warp == 7 && more) raw = raw_steps(in, row_of(cn), rows_in(cn), h);
     copy_wait<0>();
-    __syncthreads();
+    if (LEAVE == kChunks && tid < 128) sm100::bulk_wait_read_all();
+    __syncthreads();  // this chunk is there, the last one's B, x and M are free
+    if (more) {
+      fetch_tile<N, kSweepThreads>(sB0 + ((k + 1) & 1) * kTileBytes<N>, Bp + row_of(cn) * Bs, Bs, rows_in(cn), tid);
+      fetch_tile<64, kSweepThreads>(sX0 + ((k + 1) & 1) * kTileBytes<64>, Xp + row_of(cn) * Xs, Xs, rows_in(cn), tid);
+      copy_commit();
+    }
 
-    if (LEAVE == kChunks) {  // rows p of N bf16: hi, then lo
-      const long long slot64 = in.cu ? t.seq + t.start / 64 + c : (long long)t.seq * chunks + c;
-      uint32_t *o = chunk_states + ((slot64 * in.H + h) * 2) * (np / 2);
+    if constexpr (LEAVE == kChunks) {  // rows p of N bf16: hi, then lo
+      // Through shared memory and one bulk copy a row: the accumulators'
+      // layout would store 16 bytes of each 32-byte sector (114 us against
+      // 89 for both sweeps of 2 x 4096 tokens x 16 heads).
+      const uint32_t sO = smem_at(smem) + S::O;
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i)
+      for (int i = 0; i < kT; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t hi, lo;
           split2(st[i][2 * e], st[i][2 * e + 1], hi, lo);
-          const long long at = ((p0 + 8 * e) * N + 8 * i + 2 * q) / 2;
-          o[at] = hi;
-          o[np / 2 + at] = lo;
+          const uint32_t a = sO + (pw * 16 + g + 8 * e) * kRowBytes<N> + (n0 + 8 * i) * 2;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(hi) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + kTileBytes<N>), "r"(lo) : "memory");
         }
+      sm100::fence_proxy_async();
+      __syncthreads();
+      if (tid < 128) {
+        const long long slot64 = in.cu ? t.seq + t.start / 64 + c : (long long)t.seq * chunks + c;
+        const int piece = tid >> 6, p = tid & 63;
+        uint32_t *o = chunk_states + ((slot64 * in.H + h) * 2 + piece) * (np / 2) + (pt * 64 + p) * (long long)(N / 2);
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(o),
+                     "r"(sO + piece * kTileBytes<N> + p * kRowBytes<N>), "r"(N * 2)
+                     : "memory");
+        sm100::bulk_commit();
+      }
     }
 
-    float yv[4][2][4];
+    float yv[4][2][4];  // rows 16 ((i + 2 nh) mod 4) + g (+ 8): 0 and 1 stay, 2 and 3 go
     if constexpr (LEAVE == kY) {
-      // S = C B^T, rows 16 warp .. + 15, columns up to the diagonal
-      float s[8][4];
+      // M = S e^{c_i - c_j} dt_j of one or two of the ten 16 x 16 blocks on
+      // and below the diagonal, as bf16 pairs in shared memory
+#pragma unroll 1
+      for (int blk = warp; blk < 10; blk += 8) {
+        const int br = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bc = blk - br * (br + 1) / 2;
+        float s[2][2][4];  // two chains over N
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = 0.0f;
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int kk = 0; kk < N / 16; ++kk) {
-        uint32_t a[4];
-        ldsm4(block_rows<N>(sC, warp * 16, 2 * kk, lane), a);
+            for (int e = 0; e < 4; ++e) s[i][j][e] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j > warp) break;
-          uint32_t b[4];
-          ldsm4(block_cols<N>(sB, 16 * j, 2 * kk, lane), b);
-          mma16816(s[2 * j], a, b[0], b[1]);
-          mma16816(s[2 * j + 1], a, b[2], b[3]);
+        for (int kk = 0; kk < N / 16; ++kk) {
+          uint32_t a[4], b[4];
+          ldsm4(block_rows<N>(sC, 16 * br, 2 * kk, lane), a);
+          ldsm4(block_cols<N>(sB, 16 * bc, 2 * kk, lane), b);
+          mma16816(s[kk & 1][0], a, b[0], b[1]);
+          mma16816(s[kk & 1][1], a, b[2], b[3]);
+        }
+        const int r0 = 16 * br + g;
+        const float h0 = m.hi[r0], l0 = m.lo[r0], h1 = m.hi[r0 + 8], l1 = m.lo[r0 + 8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int cc = 16 * bc + 8 * j + 2 * q;
+          const float2 hj = *reinterpret_cast<const float2 *>(&m.hi[cc]);
+          const float2 lj = *reinterpret_cast<const float2 *>(&m.lo[cc]);
+          const float2 dj = *reinterpret_cast<const float2 *>(&m.dt[cc]);
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = s[0][j][e] + s[1][j][e];
+          v[0] = r0 >= cc ? v[0] * exp2_fast((h0 - hj.x) + (l0 - lj.x)) * dj.x : 0.0f;
+          v[1] = r0 > cc ? v[1] * exp2_fast((h0 - hj.y) + (l0 - lj.y)) * dj.y : 0.0f;
+          v[2] = r0 + 8 >= cc ? v[2] * exp2_fast((h1 - hj.x) + (l1 - lj.x)) * dj.x : 0.0f;
+          v[3] = r0 + 8 > cc ? v[3] * exp2_fast((h1 - hj.y) + (l1 - lj.y)) * dj.y : 0.0f;
+          uint32_t hi, lo;
+          const uint32_t at0 = tile_at<64>(sM, r0, cc / 8) + q * 4;
+          split2(v[0], v[1], hi, lo);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0), "r"(hi) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0 + kTileBytes<64>), "r"(lo) : "memory");
+          split2(v[2], v[3], hi, lo);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0 + 8 * kRowBytes<64>), "r"(hi) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0 + 8 * kRowBytes<64> + kTileBytes<64>), "r"(lo) : "memory");
         }
       }
-      // M as bf16 pairs in shared memory
-      const int r0 = warp * 16 + g;
-      const float h0 = m.hi[r0], l0 = m.lo[r0], h1 = m.hi[r0 + 8], l1 = m.lo[r0 + 8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j > 2 * warp + 1) break;
-        const int cc = 8 * j + 2 * q;
-        const float2 hj = *reinterpret_cast<const float2 *>(&m.hi[cc]);
-        const float2 lj = *reinterpret_cast<const float2 *>(&m.lo[cc]);
-        const float2 dj = *reinterpret_cast<const float2 *>(&m.dt[cc]);
-        const float v0 = r0 >= cc ? s[j][0] * exp2_fast((h0 - hj.x) + (l0 - lj.x)) * dj.x : 0.0f;
-        const float v1 = r0 > cc ? s[j][1] * exp2_fast((h0 - hj.y) + (l0 - lj.y)) * dj.y : 0.0f;
-        const float v2 = r0 + 8 >= cc ? s[j][2] * exp2_fast((h1 - hj.x) + (l1 - lj.x)) * dj.x : 0.0f;
-        const float v3 = r0 + 8 > cc ? s[j][3] * exp2_fast((h1 - hj.y) + (l1 - lj.y)) * dj.y : 0.0f;
-        uint32_t hi, lo;
-        const uint32_t at0 = tile_at<64>(sM, r0, j) + q * 4, at1 = tile_at<64>(sM, r0 + 8, j) + q * 4;
-        split2(v0, v1, hi, lo);
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0), "r"(hi) : "memory");
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0 + 8192), "r"(lo) : "memory");
-        split2(v2, v3, hi, lo);
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at1), "r"(hi) : "memory");
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at1 + 8192), "r"(lo) : "memory");
-      }
-      // the first warp has the fewest columns of S: it forms the next chunk's decays
-      if (warp == 0 && more) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
-      // C S_0, the state's pieces straight from the accumulators
+      if (warp == 7 && more) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
+      // C S_0 over this warp's half of N, the state's pieces straight from
+      // the accumulators
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -351,65 +447,67 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
 #pragma unroll
           for (int e = 0; e < 4; ++e) yv[i][j][e] = 0.0f;
 #pragma unroll
-      for (int kk = 0; kk < N / 16; ++kk) {
+      for (int kk = 0; kk < N / 32; ++kk) {
         uint32_t hb[2][2], lb[2][2];  // [8 columns of P][k half]
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             split2(st[2 * kk + u][2 * e], st[2 * kk + u][2 * e + 1], hb[e][u], lb[e][u]);
-        // eight products between two of one accumulator
-        uint32_t a[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ldsm4(block_rows<N>(sC, 16 * i, 2 * kk, lane), a[i]);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a[4];
+          ldsm4(block_rows<N>(sC, 16 * ((i + 2 * nh) & 3), nh * (N / 16) + 2 * kk, lane), a);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int e = 0; e < 2; ++e) mma16816(yv[i][e], a, hb[e][0], hb[e][1]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) mma16816(yv[i][e], a[i], hb[e][0], hb[e][1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) mma16816(yv[i][e], a[i], lb[e][0], lb[e][1]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float ga = m.gam[16 * i + g], gb = m.gam[16 * i + g + 8];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          yv[i][j][0] *= ga;
-          yv[i][j][1] *= ga;
-          yv[i][j][2] *= gb;
-          yv[i][j][3] *= gb;
+          for (int e = 0; e < 2; ++e) mma16816(yv[i][e], a, lb[e][0], lb[e][1]);
         }
       }
-      __syncthreads();  // M is there, C is free
+      float *ex = reinterpret_cast<float *>(smem + S::E);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ex[(warp * 16 + i * 8 + j * 4 + e) * 32 + lane] = yv[2 + i][j][e];
+      __syncthreads();  // M and the halves are there, C is free
       if (more) {
-        fetch_tile<N, 128>(sC, in.C + grp * N + row_of(cn) * in.cs, in.cs, rows_in(cn), tid);
+        fetch_tile<N, kSweepThreads>(sC, in.C + grp * N + row_of(cn) * in.cs, in.cs, rows_in(cn), tid);
         copy_commit();
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 16 * (i + 2 * nh) + g;
+        const float ga = m.gam[r], gb = m.gam[r + 8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            yv[i][j][e] = (yv[i][j][e] + ex[((warp ^ 4) * 16 + i * 8 + j * 4 + e) * 32 + lane]) * (e < 2 ? ga : gb);
       }
     }
 
     // the state's decay, then both products that read x
     const float all = m.all;
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st[i][e] *= all;
+    for (int i = 0; i < kT; ++i) scale4(st[i], all);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t x[4];  // (p, p + 8) x (j, j + 8) of x^T
-      ldsm4t(tile_at<64>(sX, 16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)), x);
+      ldsm4t(block_cols<64>(sX, 16 * j, 2 * pw, lane), x);
       if constexpr (LEAVE == kY) {
 #pragma unroll
-        for (int piece = 0; piece < 2; ++piece)
+        for (int i = 0; i < 2; ++i) {
+          if (j > i + 2 * nh) continue;  // above the diagonal
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i < j) continue;  // above the diagonal
+          for (int piece = 0; piece < 2; ++piece) {
             uint32_t a[4];
-            ldsm4(block_rows<64>(sM + piece * 8192, 16 * i, 2 * j, lane), a);
+            ldsm4(block_rows<64>(sM + piece * kTileBytes<64>, 16 * (i + 2 * nh), 2 * j, lane), a);
             mma16816(yv[i][0], a, x[0], x[2]);
             mma16816(yv[i][1], a, x[1], x[3]);
           }
+        }
       }
       const float *wv = REV ? m.gam : m.w;
       const float2 wa = *reinterpret_cast<const float2 *>(wv + 16 * j + 2 * q);
@@ -423,10 +521,10 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
         split3(lo * w.x, hi * w.y, u0[e], u1[e], u2[e]);
       }
 #pragma unroll
-      for (int i = 0; i < N / 16; i += 2) {
+      for (int i = 0; i < kT / 2; i += 2) {
         uint32_t b[2][4];  // (j, j + 8) x (n, n + 8)
-        ldsm4t(block_rows<N>(sB, 16 * j, 2 * i, lane), b[0]);
-        ldsm4t(block_rows<N>(sB, 16 * j, 2 * i + 2, lane), b[1]);
+        ldsm4t(block_rows<N>(sB, 16 * j, nh * (N / 16) + 2 * i, lane), b[0]);
+        ldsm4t(block_rows<N>(sB, 16 * j, nh * (N / 16) + 2 * i + 2, lane), b[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           mma16816(st[2 * (i + e)], u0, b[e][0], b[e][1]);
@@ -447,32 +545,28 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
     if (LEAVE == kEnds) run_decay *= all;
     if constexpr (LEAVE == kY) {
       const int n = rows_in(c);
-      const long long row0 = row_of(c);
+      __nv_bfloat16 *yo = y + (row_of(c) * in.H + h) * in.P + pt * 64 + pw * 16 + 2 * q;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * (i + 2 * nh) + g + 8 * e;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 16 * i + g + 8 * e;
+          for (int j = 0; j < 2; ++j) {
             uint32_t xr;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(xr) : "r"(tile_at<64>(sX, r, 2 * warp + j) + q * 4));
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(xr) : "r"(tile_at<64>(sX, r, 2 * pw + j) + q * 4));
             float xa, xb;
             bf2_get(xr, xa, xb);
             if (r < n)
-              *reinterpret_cast<uint32_t *>(y + ((row0 + r) * in.H + h) * in.P + pt * 64 + warp * 16 + 8 * j + 2 * q) =
+              *reinterpret_cast<uint32_t *>(yo + (long long)r * in.H * in.P + 8 * j) =
                   bf2_set(fmaf(Dh, xa, yv[i][j][2 * e]), fmaf(Dh, xb, yv[i][j][2 * e + 1]));
           }
+        }
     }
-    if (more) {
-      if (LEAVE != kY && warp == 0) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
-      __syncthreads();  // B, x and M are free
-      fetch_tile<N, 128>(sB, Bp + row_of(cn) * Bs, Bs, rows_in(cn), tid);
-      fetch_tile<64, 128>(sX, Xp + row_of(cn) * Xs, Xs, rows_in(cn), tid);
-      copy_commit();
-    }
+    if (more && LEAVE != kY && warp == 7) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
   }
 
+  if (LEAVE == kChunks && tid < 128) sm100::bulk_wait_all();
   float *dst = nullptr;
   if (LEAVE == kEnds) {
     dst = ends.state + (slot * in.H + h) * np + p0;
@@ -482,11 +576,36 @@ sweep_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ d
   }
   if (dst) {
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i)
+    for (int i = 0; i < kT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        dst[(8 * i + 2 * q + (e & 1)) * (long long)in.P + (e >> 1) * 8] = st[i][e];
+      for (int e = 0; e < 4; ++e) dst[at(i, e)] = st[i][e];
   }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kSweepThreads, 2)
+scan_mma_kernel(const In<__nv_bfloat16> in, int seg_chunks, Ends ends, __nv_bfloat16 *__restrict__ y,
+                float *state_out, unsigned *err) {
+  sweep_run<N, kY, false>(in, nullptr, in.state_in, seg_chunks, ends, y, state_out, nullptr, err);
+}
+template <int N>
+__global__ void __launch_bounds__(kSweepThreads, 2)
+ends_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ dy, int seg_chunks, Ends fwd,
+                Ends rev, unsigned *err) {
+  if (blockIdx.y == 0) sweep_run<N, kEnds, false>(in, nullptr, nullptr, seg_chunks, fwd, nullptr, nullptr, nullptr, err);
+  else sweep_run<N, kEnds, true>(in, dy, nullptr, seg_chunks, rev, nullptr, nullptr, nullptr, err);
+}
+// The gradient's two sweeps, side by side.
+template <int N>
+__global__ void __launch_bounds__(kSweepThreads, 2)
+boundaries_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restrict__ dy,
+                      const float *__restrict__ dstate_out, int seg_chunks, Ends fwd, Ends rev,
+                      uint32_t *__restrict__ states, uint32_t *__restrict__ adjoints, float *dstate_in,
+                      unsigned *err) {
+  if (blockIdx.y == 0)
+    sweep_run<N, kChunks, false>(in, nullptr, in.state_in, seg_chunks, fwd, nullptr, nullptr, states, err);
+  else
+    sweep_run<N, kChunks, true>(in, dy, dstate_out, seg_chunks, rev, nullptr, dstate_in, adjoints, err);
 }
 
 }  // namespace scan
