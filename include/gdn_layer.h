@@ -82,6 +82,8 @@ gdn_status gdn_conv_backward(const void *x, int64_t x_stride, const float *weigh
  * the layout of gdn_prefill's (key rows, value columns): state_in or NULL for
  * zeros, state_out may alias state_in exactly; an empty sequence passes its
  * state through.
+ * bf16 calls work on 64-token chunks: a NaN or an infinity in x, B or C can
+ * reach the outputs of the tokens before it in its chunk, and those behind it.
  * P, N in {64, 128}; H a multiple of G.  x, B, C, y and the states 16-byte
  * aligned, the strides of x, B and C multiples of 16 bytes; dt_raw
  * element-aligned with any stride.

@@ -4,7 +4,8 @@
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+import functools
+import inspect
 
 import torch
 
@@ -41,25 +42,28 @@ _declare()
 # ------------------------------------------------------------------ checks ----
 # Single-token calls are as short as their launch: messages are formatted
 # only when they are raised, and the device is switched only when it differs.
-def _device(*ts) -> torch.device:
-    dev = None
+def _device(*ts) -> int:
+    """The index of the one CUDA device that holds every given tensor."""
+    dev = -1
     for t in ts:
         if t is None:
             continue
-        d = t.device
-        if dev is None:
-            if d.type != "cuda":
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
                 raise ValueError("tensors must be CUDA tensors")
+            if dev >= 0:
+                raise ValueError(f"tensors on different devices (cuda:{dev} and cuda:{d})")
             dev = d
-        elif d != dev:
-            raise ValueError(f"tensors on different devices ({dev} and {d})")
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
     return dev
 
 
-def _call(f, name: str, dev: torch.device, stream, *args) -> None:
+def _call(f, name: str, dev: int, stream, *args) -> None:
     """The C call on ``dev`` and on ``stream`` (default: the current stream
     of ``dev``)."""
-    if dev.index == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         status = f(*args, _handle(stream, dev))
     else:
         with torch.cuda.device(dev):
@@ -74,8 +78,8 @@ _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _handle(stream, dev) -> int:
-    return _current_raw(dev.index) if stream is None else stream.cuda_stream
+def _handle(stream, dev: int) -> int:
+    return _current_raw(dev) if stream is None else stream.cuda_stream
 
 
 def _ptr(t):
@@ -92,8 +96,13 @@ def _token_stride(t: torch.Tensor, inner: int, name: str) -> int:
     """Elements between consecutive tokens of ``t``, whose last ``inner``
     dimensions are one token's contiguous row and whose leading ones are the
     tokens, equally far apart (a slice of a projection's output qualifies)."""
-    shape, strides = t.shape, t.stride()
-    row, d = 1, len(shape) - 1
+    shape = t.shape
+    if t.is_contiguous():
+        row = 1
+        for d in shape[len(shape) - inner:]:
+            row *= d
+        return row
+    strides, row = t.stride(), 1
     for d in range(len(shape) - 1, len(shape) - 1 - inner, -1):
         if shape[d] != 1 and strides[d] != row:
             raise ValueError(f"{name}: a token's row must be contiguous")
@@ -129,9 +138,37 @@ def _sequences(lead, cu_seqlens):
     return cu_seqlens.numel() - 1, lead[1]
 
 
+def _streamed(f):
+    """With a ``stream``, the whole call runs with it as the current one: the
+    outputs and the workspace made here are then that stream's, and none of
+    them is memory that another stream still works on."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        if len(args) > at:
+            kw["stream"], args = args[at], args[:at]
+        stream = kw.pop("stream", None) if kw else None
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+def _new(shape, dtype, x, like):
+    """An output on x's device; like ``like``, where a tensor of its shape
+    and type is at hand (torch makes those in half the time).  The inputs that
+    outputs are made like of are contiguous or refused, slices apart, whose
+    likes are contiguous."""
+    if like is not None and like.shape == shape and like.dtype == dtype:
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=x.device)
+
+
 def _scratch(need: int, workspace, dev):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev)) if need else None
     _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(),
           "workspace must be a contiguous uint8 tensor")
     return workspace
@@ -173,6 +210,7 @@ def gdn_conv_prefill_into(x, weight, bias, state_in, cu_seqlens, y, state_out,
           GDN_ACT[activation], _ptr(y), _ptr(state_out))
 
 
+@_streamed
 def gdn_conv_prefill(x, weight, bias=None, state_in=None, cu_seqlens=None,
                      activation: str = "silu", stream=None):
     """Causal convolution of every channel: x [B, T, C] (packed: [1, T, C]
@@ -180,9 +218,8 @@ def gdn_conv_prefill(x, weight, bias=None, state_in=None, cu_seqlens=None,
     fp32 [C], state [n_seq, W - 1, C] (the last inputs, oldest first).  x may
     be a slice of wider rows.  Returns ``(y, state_out)``."""
     n, _ = _sequences(x.shape[:2], cu_seqlens)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    state_out = torch.empty((n, weight.shape[-1] - 1, x.shape[-1]), dtype=x.dtype,
-                            device=x.device)
+    y = torch.empty_like(x)
+    state_out = _new((n, weight.shape[-1] - 1, x.shape[-1]), x.dtype, x, state_in)
     gdn_conv_prefill_into(x, weight, bias, state_in, cu_seqlens, y, state_out, activation, stream)
     return y, state_out
 
@@ -200,12 +237,14 @@ def gdn_conv_decode_into(x, weight, bias, state, y, activation: str = "silu",
           _ptr(y))
 
 
+@_streamed
 def gdn_conv_decode(x, weight, bias, state, activation: str = "silu", stream=None):
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = torch.empty_like(x)
     gdn_conv_decode_into(x, weight, bias, state, y, activation, stream)
     return y
 
 
+@_streamed
 def gdn_conv_backward(x, weight, dy, bias=None, state_in=None, cu_seqlens=None,
                       dstate_out=None, activation: str = "silu", workspace=None, stream=None):
     """Gradients of ``gdn_conv_prefill(x, weight, bias, state_in, cu_seqlens)``
@@ -220,10 +259,10 @@ def gdn_conv_backward(x, weight, dy, bias=None, state_in=None, cu_seqlens=None,
     _like(dy, x, "dy")
     need = int(lib.gdn_conv_backward_workspace_bytes(n, T, C, W, int(cu_seqlens is not None)))
     ws = _scratch(need, workspace, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dw = torch.empty((C, W), dtype=torch.float32, device=dev)
-    db = torch.empty((C,), dtype=torch.float32, device=dev)
-    ds = torch.empty(shape, dtype=x.dtype, device=dev)
+    dx = torch.empty_like(x)
+    dw = torch.empty_like(weight)
+    db = _new((C,), torch.float32, x, bias)
+    ds = _new(shape, x.dtype, x, state_in)
     _call(lib.gdn_conv_backward, "gdn_conv_backward", dev, stream, _ptr(x), xs, _ptr(weight),
           _ptr(bias), _ptr(state_in), _ptr(cu_seqlens), n, T, C, W, GDN_DTYPE[x.dtype],
           GDN_ACT[activation], _ptr(dy), _ptr(dstate_out), _ptr(ws), 0 if ws is None else
@@ -252,6 +291,7 @@ def _scan_args(x, dt, A, B, C, D, dt_bias, lead: int, name):
     return H, P, G, N, args
 
 
+@_streamed
 def gdn_scan_prefill_into(x, dt, A, B, C, D, dt_bias, state_in, cu_seqlens, y, state_out,
                           workspace=None, stream=None) -> None:
     """gdn_scan_prefill into preallocated ``y`` and ``state_out`` (which may
@@ -272,6 +312,7 @@ def gdn_scan_prefill_into(x, dt, A, B, C, D, dt_bias, state_in, cu_seqlens, y, s
           ws.numel(), _ptr(y), _ptr(state_out))
 
 
+@_streamed
 def gdn_scan_prefill(x, dt, A, B, C, D=None, dt_bias=None, state_in=None, cu_seqlens=None,
                      workspace=None, stream=None):
     """Selective state space scan, one decay a head: x [B, T, H, P], dt
@@ -280,9 +321,8 @@ def gdn_scan_prefill(x, dt, A, B, C, D=None, dt_bias=None, state_in=None, cu_seq
     wider rows; A, D, dt_bias fp32 [H]; states fp32 [n_seq, H, N, P].
     Returns ``(y, state_out)``."""
     n, _ = _sequences(x.shape[:2], cu_seqlens)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    state_out = torch.empty((n, x.shape[2], B.shape[-1], x.shape[3]), dtype=torch.float32,
-                            device=x.device)
+    y = torch.empty_like(x)
+    state_out = _new((n, x.shape[2], B.shape[-1], x.shape[3]), torch.float32, x, state_in)
     gdn_scan_prefill_into(x, dt, A, B, C, D, dt_bias, state_in, cu_seqlens, y, state_out,
                           workspace, stream)
     return y, state_out
@@ -301,12 +341,14 @@ def gdn_scan_decode_into(x, dt, A, B, C, state, y, D=None, dt_bias=None, stream=
           N, GDN_DTYPE[x.dtype], _ptr(y))
 
 
+@_streamed
 def gdn_scan_decode(x, dt, A, B, C, state, D=None, dt_bias=None, stream=None):
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = torch.empty_like(x)
     gdn_scan_decode_into(x, dt, A, B, C, state, y, D, dt_bias, stream)
     return y
 
 
+@_streamed
 def gdn_scan_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, state_in=None, cu_seqlens=None,
                       dstate_out=None, workspace=None, stream=None):
     """Gradients of ``gdn_scan_prefill`` for ``dy`` (y's shape and dtype) and
@@ -321,11 +363,10 @@ def gdn_scan_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, state_in=None, c
     need = int(lib.gdn_scan_backward_workspace_bytes(n, T, H, P, G, N, GDN_DTYPE[x.dtype],
                                                      int(cu_seqlens is not None)))
     ws = _scratch(need, workspace, dev)
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
-    dx, ddt = new(x.shape, x.dtype), new(dt.shape, x.dtype)
-    dB, dC = new(B.shape, x.dtype), new(B.shape, x.dtype)
-    dA, dD, db = (new((H,), torch.float32) for _ in range(3))
-    ds = new((n, H, N, P), torch.float32)
+    dx, ddt = torch.empty_like(x), torch.empty_like(dt)
+    dB, dC = torch.empty_like(B), torch.empty_like(B)
+    dA, dD, db = torch.empty_like(A), torch.empty_like(A), torch.empty_like(A)
+    ds = _new((n, H, N, P), torch.float32, x, state_in)
     _call(lib.gdn_scan_backward, "gdn_scan_backward", dev, stream, *args, _ptr(state_in),
           _ptr(cu_seqlens), n, T, H, P, G, N, GDN_DTYPE[x.dtype], _ptr(dy), _ptr(dstate_out),
           _ptr(ws), 0 if ws is None else ws.numel(), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB),
@@ -372,6 +413,7 @@ def _norm_rows(x, *others):
     return rows // h, h, [0 if t is None else _token_stride(t, 2, "rows") for t in ts]
 
 
+@_streamed
 def gdn_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, qdq: str = "none",
              stream=None):
     """RMS norm of the rows of x [.., d]: s = x + residual (rounded to x's
@@ -387,24 +429,25 @@ def gdn_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, qdq: str = 
     d = x.shape[-1]
     _f32((d,), "weight", weight)
     tokens, heads, (xs, rs, gs) = _norm_rows(x, residual, gate)
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
     scales = None
     if qdq == "none":
-        y = new(x.shape, x.dtype)
+        y = torch.empty_like(x)
     elif qdq == "fp8_row":
-        y, scales = new(x.shape, torch.float8_e4m3fn), new(x.shape[:-1], torch.float32)
+        y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        scales = _new(x.shape[:-1], torch.float32, x, None)
     else:
         group = int(qdq.split("_g")[1])
         _need(d % group == 0, "d must be a multiple of the group")
-        y = new(x.shape, torch.int8)
-        scales = new(x.shape[:-1] + (d // group,), torch.float32)
-    s = None if residual is None else new(x.shape, x.dtype)
+        y = torch.empty_like(x, dtype=torch.int8)
+        scales = _new(x.shape[:-1] + (d // group,), torch.float32, x, None)
+    s = None if residual is None else torch.empty_like(x)
     _call(lib.gdn_norm, "gdn_norm", dev, stream, _ptr(x), xs, _ptr(residual), rs, _ptr(gate),
           gs, _ptr(weight), tokens, heads, d, float(eps), GDN_DTYPE[x.dtype], GDN_NORM_OUT[qdq],
           _ptr(y), _ptr(scales), _ptr(s))
     return (y if scales is None else QuantizedRows(y, scales, qdq)), s
 
 
+@_streamed
 def gdn_norm_backward(x, weight, dy, gate=None, dresidual=None, eps: float = 1e-6,
                       workspace=None, stream=None):
     """Gradients of ``gdn_norm`` at x (the s it returned, or its x) for
@@ -419,9 +462,9 @@ def gdn_norm_backward(x, weight, dy, gate=None, dresidual=None, eps: float = 1e-
     _need(dy is not None, "dy is needed")
     tokens, heads, (xs, ys, gs, rs) = _norm_rows(x, dy, gate, dresidual)
     ws = _scratch(int(lib.gdn_norm_backward_workspace_bytes(tokens, heads, d)), workspace, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dw = torch.empty((d,), dtype=torch.float32, device=dev)
-    dg = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dx = torch.empty_like(x)
+    dw = torch.empty_like(weight)
+    dg = None if gate is None else torch.empty_like(x)
     _call(lib.gdn_norm_backward, "gdn_norm_backward", dev, stream, _ptr(x), xs, _ptr(gate), gs,
           _ptr(weight), _ptr(dy), ys, _ptr(dresidual), rs, tokens, heads, d, float(eps),
           GDN_DTYPE[x.dtype], _ptr(ws), 0 if ws is None else ws.numel(), _ptr(dx), _ptr(dw),

@@ -91,10 +91,6 @@ Plan plan(int n_seq, int T, int H, int P, int N, bool packed, int sweeps) {
   return p;
 }
 
-template <typename K>
-bool fits(K kern, int smem) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
-}
 unsigned run_blocks(const Call &c, const Plan &p) { return (unsigned)(p.slots * c.H * (c.P / 64)); }
 
 // What the runs add, then what they start from; rev.state: backwards too.
@@ -104,7 +100,8 @@ gdn_status run_starts(const Call &c, const Plan &p, const __nv_bfloat16 *dy, con
   const In<__nv_bfloat16> in = typed<__nv_bfloat16>(c);
   constexpr int smem = (int)SweepSmem<N, kEnds>::bytes;
   const unsigned both = rev.state ? 2 : 1;
-  if (!fits(ends_mma_kernel<N>, smem)) return GDN_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(ends_mma_kernel<N>, smem, done)) return GDN_ERR_CUDA;
   ends_mma_kernel<N><<<dim3(run_blocks(c, p), both), kSweepThreads, smem, st>>>(in, dy, p.seg_chunks, fwd, rev, err);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   const long long np = (long long)c.N * c.P;
@@ -124,7 +121,8 @@ gdn_status prefill_mma(const Call &c, char *ws, void *y, float *state_out, unsig
     if (s != GDN_OK) return s;
   }
   constexpr int smem = (int)SweepSmem<N, kY>::bytes;
-  if (!fits(scan_mma_kernel<N>, smem)) return GDN_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(scan_mma_kernel<N>, smem, done)) return GDN_ERR_CUDA;
   scan_mma_kernel<N><<<run_blocks(c, p), kSweepThreads, smem, st>>>(
       in, p.seg_chunks, ends, static_cast<__nv_bfloat16 *>(y), state_out, err);
   return launched();
@@ -243,8 +241,8 @@ gdn_status backward_f32(const Call &c, const Grads &g, char *ws, unsigned *err, 
                                                              adjoints, err);
   auto kern = chunk_grad_kernel<float, N, P>;
   constexpr size_t smem = ChunkLayout<N, P>::bytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return GDN_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kern, (int)smem, done)) return GDN_ERR_CUDA;
   kern<<<(unsigned)(w.slots * c.H), 256, smem, st>>>(
       in, dy, states, adjoints, static_cast<float *>(g.dx), static_cast<float *>(g.draw),
       reinterpret_cast<float *>(ws + w.dB), reinterpret_cast<float *>(ws + w.dC),
@@ -268,14 +266,14 @@ gdn_status backward_mma(const Call &c, const Grads &g, char *ws, unsigned *err, 
     if ((s = run_starts<N>(c, w.runs, dy, g.dstate_out, fwd, rev, err, st)) != GDN_OK) return s;
   }
   constexpr int sweep_smem = (int)SweepSmem<N, kChunks>::bytes;
-  if (!fits(boundaries_mma_kernel<N>, sweep_smem)) return GDN_ERR_CUDA;
+  static std::atomic<uint64_t> sweeps_done{0}, chunks_done{0};
+  if (!allow_smem(boundaries_mma_kernel<N>, sweep_smem, sweeps_done)) return GDN_ERR_CUDA;
   boundaries_mma_kernel<N><<<dim3(run_blocks(c, w.runs), 2), kSweepThreads, sweep_smem, st>>>(
       in, dy, g.dstate_out, w.runs.seg_chunks, fwd, rev, states, adjoints, g.dstate_in, err);
   if ((s = launched()) != GDN_OK) return s;
   auto kern = chunk_grad_mma_kernel<N, P>;
   constexpr int smem = (int)GradSmem<N, P>::bytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return GDN_ERR_CUDA;
+  if (!allow_smem(kern, smem, chunks_done)) return GDN_ERR_CUDA;
   const GroupOut out{static_cast<T *>(g.dB), static_cast<T *>(g.dC), reinterpret_cast<float *>(ws + w.dB),
                      reinterpret_cast<float *>(ws + w.dC)};
   kern<<<(unsigned)(w.slots * c.G * w.splits), kGradThreads, smem, st>>>(

@@ -217,3 +217,33 @@ def test_calls_at_once_on_two_streams(cuda_lib):
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_given_stream(cuda_lib):
+    """``stream=`` and the current stream give the same bits, with outputs and
+    workspaces that belong to the stream that writes them."""
+    L = Layer(BF16)
+    g = torch.Generator().manual_seed(7)
+    x, res = (torch.randn(1, 700, D, generator=g).to(BF16).cuda() for _ in range(2))
+    r = prompt(cuda_lib, L, x, res)
+    dy = torch.randn(1, 700, H, P, generator=g).to(BF16).cuda()
+    dc = torch.randn(1, 700, XBC, generator=g).to(BF16).cuda()
+    scan = (r["u"], r["dt"], L.A, r["B"], r["C"])
+
+    def run(**kw):
+        return (cuda_lib.gdn_scan_prefill(*scan, D=L.D, **kw)
+                + cuda_lib.gdn_scan_backward(*scan, dy, D=L.D, **kw)
+                + cuda_lib.gdn_conv_prefill(r["xbc"], L.conv_w, L.conv_b, **kw)
+                + cuda_lib.gdn_conv_backward(r["xbc"], L.conv_w, dc, L.conv_b, **kw)
+                + cuda_lib.gdn_norm(x, L.w_in, residual=res, **kw)
+                + cuda_lib.gdn_norm_backward(x, L.w_in, res, **kw)[:2])
+
+    want = run()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        side.wait_stream(torch.cuda.current_stream())
+        got = run(stream=side)
+        junk = [torch.zeros(1 << 20, device="cuda") for _ in range(8)]   # the current stream's own
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        del junk
