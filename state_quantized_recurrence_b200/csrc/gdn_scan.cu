@@ -55,26 +55,26 @@ unsigned units(const Call &c) { return (unsigned)(c.n_seq * c.H * (c.P / 64)); }
 // Sequences are cut into runs of chunks where (sequence, head, 64 columns)
 // units alone would leave SMs idle: a first launch forms what each run adds
 // to a zero state, a second turns that into the state each run starts from.
-// As many runs as two CTAs on every SM: 4 x 4096 tokens x 16 heads of 128
-// take 326 us so, 345 with half as many and 336 with twice; runs of four
-// chunks at least.
+// That is half as much work again, so a call with 100 units or more goes
+// without (4 x 4096 tokens x 16 heads of 128, 128 units: 281 us, against 337
+// cut into three and 332 into nine); below, there are as many runs as two
+// CTAs on every SM, of four chunks at least (one sequence of 8191 tokens, 8
+// units: 61 us; 80 with half as many).
 struct Plan {
   int seg_chunks;   // chunks of a run
   bool split;
   long long slots;  // run slots of the call
   size_t state, decay, bytes;  // workspace parts
 };
-constexpr int kResident = 2 * 148;
-// `sweeps`: how many such launches share the device (the gradient's two).
-Plan plan(int n_seq, int T, int H, int P, int N, bool packed, int sweeps) {
+constexpr int kResident = 2 * 148, kEnough = 100;
+Plan plan(int n_seq, int T, int H, int P, int N, bool packed) {
   Plan p = {};
-  const long long target = kResident / sweeps;
   const long long units = (long long)n_seq * H * (P / 64);
   const long long chunks = (T + 63LL) / 64;
   const long long mean = packed && n_seq > 0 ? (chunks + n_seq - 1) / n_seq : chunks;
   long long seg = chunks > 0 ? chunks : 1;
-  if (units > 0 && units * 3 < target * 2 && mean > 4) {
-    const long long want = (target + units - 1) / units;
+  if (units > 0 && units < kEnough && mean > 4) {
+    const long long want = (kResident + units - 1) / units;
     long long s = (mean + want - 1) / want;
     if (s < 4) s = 4;
     if (s < seg) {
@@ -113,7 +113,7 @@ gdn_status run_starts(const Call &c, const Plan &p, const __nv_bfloat16 *dy, con
 template <int N>
 gdn_status prefill_mma(const Call &c, char *ws, void *y, float *state_out, unsigned *err, cudaStream_t st) {
   const In<__nv_bfloat16> in = typed<__nv_bfloat16>(c);
-  const Plan p = plan(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr, 1);
+  const Plan p = plan(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr);
   Ends ends{nullptr, nullptr};
   if (p.split) {
     ends = Ends{reinterpret_cast<float *>(ws + p.state), reinterpret_cast<float *>(ws + p.decay)};
@@ -136,9 +136,9 @@ gdn_status prefill(const Call &c, gdn_dtype dt, char *ws, void *y, float *state_
   const In<float> in = typed<float>(c);
   float *yo = static_cast<float *>(y);
   if (c.N == 128)
-    sweep_kernel<float, 128, kForward><<<units(c), 256, 0, st>>>(in, nullptr, nullptr, yo, state_out, nullptr, err);
+    forward_kernel<float, 128><<<units(c), 256, 0, st>>>(in, yo, state_out, err);
   else
-    sweep_kernel<float, 64, kForward><<<units(c), 256, 0, st>>>(in, nullptr, nullptr, yo, state_out, nullptr, err);
+    forward_kernel<float, 64><<<units(c), 256, 0, st>>>(in, yo, state_out, err);
   return launched();
 }
 
@@ -194,7 +194,7 @@ Workspace workspace(int n_seq, int T, int H, int P, int G, int N, gdn_dtype dt, 
   w.part = w.dC + sums;
   w.bytes = w.part + (size_t)w.slots * H * 16;
   if (mma) {
-    w.runs = plan(n_seq, T, H, P, N, packed, 2);
+    w.runs = plan(n_seq, T, H, P, N, packed);
     if (w.runs.split) {
       w.fwd = w.bytes;
       w.fwd_decay = w.fwd + w.runs.decay;
@@ -236,9 +236,9 @@ gdn_status backward_f32(const Call &c, const Grads &g, char *ws, unsigned *err, 
   float *states = reinterpret_cast<float *>(ws + w.states);
   float *adjoints = reinterpret_cast<float *>(ws + w.adjoints);
   const float *dy = static_cast<const float *>(g.dy);
-  sweep_kernel<float, N, kStates><<<units(c), 256, 0, st>>>(in, nullptr, nullptr, nullptr, nullptr, states, err);
-  sweep_kernel<float, N, kAdjoint><<<units(c), 256, 0, st>>>(in, dy, g.dstate_out, nullptr, g.dstate_in,
-                                                             adjoints, err);
+  boundaries_kernel<float, N><<<dim3(units(c), 2), 256, 0, st>>>(in, dy, g.dstate_out, states, adjoints,
+                                                                 g.dstate_in, err);
+  if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   auto kern = chunk_grad_kernel<float, N, P>;
   constexpr size_t smem = ChunkLayout<N, P>::bytes;
   static std::atomic<uint64_t> done{0};
@@ -303,7 +303,7 @@ size_t gdn_scan_prefill_workspace_bytes(int n_seq, int T, int H, int P, int G, i
   const scan::Call c{nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, nullptr, nullptr, nullptr,
                      nullptr, nullptr, 0, T, H, P, G, N};
   if (n_seq <= 0 || dtype != GDN_DTYPE_BF16 || scan::check(c, dtype, false) != GDN_OK) return 0;
-  return scan::plan(n_seq, T, H, P, N, packed != 0, 1).bytes;
+  return scan::plan(n_seq, T, H, P, N, packed != 0).bytes;
 }
 
 gdn_status gdn_scan_prefill(const void *x, int64_t x_stride, const void *dt_raw,

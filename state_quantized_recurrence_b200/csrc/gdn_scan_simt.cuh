@@ -43,9 +43,9 @@ enum Sweep : int { kForward = 0, kStates = 1, kAdjoint = 2 };
 constexpr int kTok = 16;  // tokens staged at a time
 
 template <typename T, int N, int MODE>
-__global__ void __launch_bounds__(256)
-sweep_kernel(const In<T> in, const T *__restrict__ dy, const float *__restrict__ last,
-             T *__restrict__ y, float *out_state, float *__restrict__ dump, unsigned *err) {
+__device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
+                                      const float *__restrict__ last, T *__restrict__ y,
+                                      float *out_state, float *__restrict__ dump, unsigned *err) {
   constexpr int R = N / 4;
   __shared__ __align__(16) float sb[kTok][N], sc[kTok][N], su[kTok][64], sy[4][kTok][64];
   __shared__ float sa[kTok], sdt[kTok];
@@ -151,6 +151,21 @@ sweep_kernel(const In<T> in, const T *__restrict__ dy, const float *__restrict__
 #pragma unroll
     for (int i = 0; i < R; ++i) out_state[at + (long long)(q * R + i) * in.P] = st[i];
   }
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(256)
+forward_kernel(const In<T> in, T *__restrict__ y, float *out_state, unsigned *err) {
+  sweep<T, N, kForward>(in, nullptr, nullptr, y, out_state, nullptr, err);
+}
+// The gradient's two sweeps, side by side: a sweep is a chain of tokens that
+// leaves most of an SM idle.
+template <typename T, int N>
+__global__ void __launch_bounds__(256)
+boundaries_kernel(const In<T> in, const T *__restrict__ dy, const float *__restrict__ dstate_out,
+                  float *__restrict__ states, float *__restrict__ adjoints, float *dstate_in, unsigned *err) {
+  if (blockIdx.y == 0) sweep<T, N, kStates>(in, nullptr, nullptr, nullptr, nullptr, states, err);
+  else sweep<T, N, kAdjoint>(in, dy, dstate_out, nullptr, dstate_in, adjoints, err);
 }
 
 // One decode token of one (sequence, head, 64-column tile).  Bound by the
@@ -275,7 +290,10 @@ struct ChunkLayout {
   static constexpr int bn = N + 4, bp = P + 4, bl = kChunk + 1;
   static constexpr int B = 0, C = B + kChunk * bn, X = C + kChunk * bn, DY = X + kChunk * bp;
   static constexpr int M = DY + kChunk * bp, W = M + kChunk * bl, Z = W + kChunk * bl;
-  static constexpr int floats = Z + kChunk * bl;
+  // sixteen columns of a state at a time, rows 17 apart: reading a column of
+  // it from global memory row by row took half of the kernel's time
+  static constexpr int S = Z + kChunk * bl;
+  static constexpr int floats = S + N * 17;
   static constexpr size_t bytes = floats * 4 + sizeof(ChunkSmem) + 16;
 };
 
@@ -283,6 +301,18 @@ __device__ __forceinline__ float half_sum(float v) {  // over 16 neighbouring la
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Columns k0 .. k0 + 15 of a state [N][P] into rows of 17, by 256 threads.
+template <int N, int P>
+__device__ __forceinline__ void stage_columns(const float *__restrict__ state, int k0, float *s) {
+  __syncthreads();  // the last ones have been read
+  for (int i = threadIdx.x; i < N * 4; i += 256) {
+    const float4 v = __ldg(reinterpret_cast<const float4 *>(state + (long long)(i / 4) * P + k0 + i % 4 * 4));
+    float *d = s + (i / 4) * 17 + i % 4 * 4;
+    d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+  }
+  __syncthreads();
 }
 
 template <typename T, int N, int P>
@@ -293,7 +323,7 @@ chunk_grad_kernel(const In<T> in, const T *__restrict__ dy, const float *__restr
   using L = ChunkLayout<N, P>;
   extern __shared__ __align__(16) float sm[];
   float *sB = sm + L::B, *sC = sm + L::C, *sX = sm + L::X, *sY = sm + L::DY;
-  float *sM = sm + L::M, *sW = sm + L::W, *sZ = sm + L::Z;
+  float *sM = sm + L::M, *sW = sm + L::W, *sZ = sm + L::Z, *sS = sm + L::S;
   ChunkSmem &m = *reinterpret_cast<ChunkSmem *>(
       (reinterpret_cast<uintptr_t>(sm + L::floats) + 7) & ~uintptr_t(7));
   const int tid = threadIdx.x, h = blockIdx.x % in.H, g = h / (in.H / in.G);
@@ -427,9 +457,10 @@ chunk_grad_kernel(const In<T> in, const T *__restrict__ dy, const float *__restr
       }
     }
     for (int k = 0; k < P; ++k) {
+      if (k % 16 == 0) stage_columns<N, P>(H0, k, sS);
       float b[J];
 #pragma unroll
-      for (int j = 0; j < J; ++j) b[j] = __ldg(H0 + (long long)(tx + 16 * j) * P + k);
+      for (int j = 0; j < J; ++j) b[j] = sS[(tx + 16 * j) * 17 + k % 16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = sY[(ty + 16 * i) * L::bp + k];
@@ -468,9 +499,10 @@ chunk_grad_kernel(const In<T> in, const T *__restrict__ dy, const float *__restr
       }
     }
     for (int k = 0; k < P; ++k) {
+      if (k % 16 == 0) stage_columns<N, P>(Gn, k, sS);
       float b[J];
 #pragma unroll
-      for (int j = 0; j < J; ++j) b[j] = __ldg(Gn + (long long)(tx + 16 * j) * P + k);
+      for (int j = 0; j < J; ++j) b[j] = sS[(tx + 16 * j) * 17 + k % 16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = sX[(ty + 16 * i) * L::bp + k];
