@@ -151,8 +151,8 @@ gdn_status decode(const Call &c, float *state, void *y, cudaStream_t st) {
 }
 
 // The gradient's workspace, every part a multiple of 16 bytes: the state at
-// every chunk's start and its adjoint at every chunk's end (fp32, or two bf16
-// pieces), dB and dC of every head (fp32) or of every share of a group's
+// every chunk's start and its adjoint at every chunk's end (fp32, or three
+// bf16 pieces), dB and dC of every head (fp32) or of every share of a group's
 // heads (bf16, where there are several), the heads' parameters' parts of
 // every chunk, and for bf16 what runs of chunks hand over.
 struct Workspace {
@@ -186,7 +186,7 @@ Workspace workspace(int n_seq, int T, int H, int P, int G, int N, gdn_dtype dt, 
   w.slots = layer::slot_count(n_seq, T, kChunk, packed);
   w.rows = packed ? T : (long long)n_seq * T;
   w.splits = mma ? head_splits(w.slots * G, H / G) : H / G;
-  const size_t states = (size_t)w.slots * H * N * P * 4;
+  const size_t states = (size_t)w.slots * H * N * P * (mma ? 2 * kPieces : 4);
   const size_t sums = mma && w.splits == 1 ? 0 : (size_t)w.rows * G * w.splits * N * 4;
   w.adjoints = states;
   w.dB = w.adjoints + states;

@@ -6,8 +6,16 @@
 // S = C B^T is formed once; dB and dC are summed over the heads in the
 // accumulators, so that neither leaves the SM before it is whole (with the
 // heads split over several CTAs, their fp32 parts are added afterwards in
-// order).  Bound by the legacy tensor rate (1024 multiply-adds a clock and
-// SM) of some six million multiply-adds a head and chunk at N = 128, P = 64.
+// order).
+//
+// 2 x 4096 tokens x 16 heads, N = 128, P = 64: 188 us, 22 thousand cycles a
+// head and chunk, of which the tensor pipe is busy 5.4 (24 %), the shared
+// memory pipe 49 %; the rest is the latency of four dependent stages between
+// barriers.  Eight warps with twice the tile ran the same (181 us).
+//
+// dA and ddt_bias add up e^{c_i} C_i . H0 dy_i, dt_j e^{..} B_j . G x_j and
+// <G, H0>, whose states enter as bf16 pairs: a few 1e-6 relative.  The part
+// inside a chunk (Z) is fp32 throughout.
 #pragma once
 
 #include "gdn_scan_mma.cuh"
@@ -25,10 +33,15 @@ struct GradSmem {
   static constexpr uint32_t M = G + 2 * kTileBytes<N>;     // hi, lo
   static constexpr uint32_t W = M + 2 * kTileBytes<64>;
   static constexpr uint32_t Z = W + 2 * kTileBytes<64>;    // fp32 [64][65]
-  static constexpr uint32_t V = (Z + 64 * 65 * 4 + 15) / 16 * 16;
-  // row sums by warp column: r, q, x . du (4 each), Z block sums [4][64], l, gh and dD by warp
+  static constexpr uint32_t kZ = 64 * 65 * 4 > kTileBytes<N> ? 64 * 65 * 4 : kTileBytes<N>;
+  static constexpr uint32_t V = (Z + kZ + 15) / 16 * 16;
+  // the third pieces of H and G take the places of W and Z once those are read
+  static constexpr uint32_t H3 = W, G3 = Z;
+  static_assert(kTileBytes<N> <= 2 * kTileBytes<64>, "H's third piece fits into W");
+  // row sums by warp column: r, q (4 each), Z block sums [4][64], Z's part of
+  // l, l, gh and dD by warp
   struct Rows {
-    float r[4][64], q[4][64], xdu[4][64], zb[4][64], l[64], gh[16], dD[16];
+    float r[4][64], q[4][64], zb[4][64], lz[64], l[64], gh[16], dD[16];
   };
   static constexpr uint32_t D = V + (sizeof(Rows) + 15) / 16 * 16;
   static constexpr uint32_t bytes = D + 2 * sizeof(Decays);
@@ -81,12 +94,15 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
   const long long np = (long long)N * in.P;
 
   auto fetch_states = [&](int h, int pt) {
-    const __nv_bfloat16 *s = states + (slot * in.H + h) * 2 * np + (long long)pt * 64 * N;
-    const __nv_bfloat16 *a = adjoints + (slot * in.H + h) * 2 * np + (long long)pt * 64 * N;
+    const __nv_bfloat16 *s = states + (slot * in.H + h) * kPieces * np + (long long)pt * 64 * N;
+    const __nv_bfloat16 *a = adjoints + (slot * in.H + h) * kPieces * np + (long long)pt * 64 * N;
     fetch_tile<N, kGradThreads>(sH, s, N, 64, tid);
     fetch_tile<N, kGradThreads>(sH + kTileBytes<N>, s + np, N, 64, tid);
     fetch_tile<N, kGradThreads>(sG, a, N, 64, tid);
     fetch_tile<N, kGradThreads>(sG + kTileBytes<N>, a + np, N, 64, tid);
+  };
+  auto fetch_third = [&](const __nv_bfloat16 *from, uint32_t to, int h, int pt) {
+    fetch_tile<N, kGradThreads>(to, from + ((slot * in.H + h) * kPieces + 2) * np + (long long)pt * 64 * N, N, 64, tid);
   };
   auto fetch_head = [&](int h) {
 #pragma unroll
@@ -166,7 +182,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
             if (r == c + u) dD += k;
             mv[u] = s * d;
             wv[u] = k * d * m.dt[c + u];
-            sZ[r * 65 + c + u] = s * wv[u];
+            sZ[r * 65 + c + u] = mv[u] * k;
           }
           uint32_t hi, lo;
           const uint32_t at = tile_at<64>(0, r, c / 8) + q * 4;
@@ -237,75 +253,88 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
         }
       }
     }
-    float rsum[1][2] = {{0.f, 0.f}}, qsum[1][2] = {{0.f, 0.f}}, xsum[1][2] = {{0.f, 0.f}};
+    __syncthreads();  // Z's sums are there, W has been read
+    fetch_third(states, base + L::H3, h, 0);
+    copy_commit();
+    if (tid < 256) {  // Z's part of l_t, four threads a token
+      const int tt = tid >> 2, b = tid & 3;
+      float s = 0.0f;
+      for (int c = 16 * b; c < min(16 * b + 16, tt); ++c) {
+        float v = sZ[tt * 65 + c];
+        for (int k = tt / 16 + 1; k < 4; ++k) v += rs.zb[k][c];
+        s = fmaf(m.dt[c], v, s);
+      }
+      s = quad_sum(s);
+      if (b == 0) rs.lz[tt] = s;
+    }
+    float rsum[2] = {0.f, 0.f}, qsum[2] = {0.f, 0.f};
     const float Dh = in.D ? in.D[h] : 0.0f;
+    // T = dy H0 (side 0) or x G (side 1) from `pieces` tiles at tS; its
+    // scaled rows join dC or dB, their products with C or B the row sums
+    auto with_state = [&](int side, uint32_t tA, uint32_t tS, int pieces) {
+      const uint32_t tO = side ? sB : sC;
+      float T[2 * kJ][4];
+#pragma unroll
+      for (int j = 0; j < 2 * kJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) T[j][e] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t a[4];
+        ldsm4(block_rows<64>(tA, gr, 2 * kk, lane), a);
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece) {
+          if (piece >= pieces) break;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            uint32_t b[4];
+            ldsm4t(block_rows<N>(tS + piece * kTileBytes<N>, 16 * kk, gc / 8 + 2 * j, lane), b);
+            mma16816(T[2 * j], a, b[0], b[1]);
+            mma16816(T[2 * j + 1], a, b[2], b[3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = gr + g + 8 * e;
+        const float f = side ? m.w[r] : m.gam[r];
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2 * kJ; ++j) {
+          uint32_t o;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o) : "r"(tile_at<N>(tO, r, gc / 8 + j) + q * 4));
+          float oa, ob;
+          bf2_get(o, oa, ob);
+          const float ta = T[j][2 * e], tb = T[j][2 * e + 1];
+          s = fmaf(oa, ta, fmaf(ob, tb, s));
+          float(&acc)[4] = side ? aB[0][j] : aC[0][j];
+          acc[2 * e] = fmaf(f, ta, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(f, tb, acc[2 * e + 1]);
+        }
+        if (side) qsum[e] = fmaf(m.del[r], s, qsum[e]);
+        else rsum[e] = fmaf(m.gam[r], s, rsum[e]);
+      }
+    };
 #pragma unroll 1
     for (int pt = 0; pt < kPT; ++pt) {
       const uint32_t tX = sX + pt * kTileBytes<64>, tY = sY + pt * kTileBytes<64>;
       if (pt > 0) {
         __syncthreads();  // the first tile's states have been read
         fetch_states(h, pt);
+        fetch_third(states, base + L::H3, h, pt);
+        fetch_third(adjoints, base + L::G3, h, pt);
         copy_commit();
         copy_wait<0>();
         __syncthreads();
       }
-      // dC += e^{c_i} dy H0 and its products with C; then dB with x and G
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        const uint32_t tA = side ? tX : tY, tS = side ? sG : sH, tO = side ? sB : sC;
-        float T[1][2 * kJ][4];
-#pragma unroll
-        for (int i = 0; i < 1; ++i)
-#pragma unroll
-          for (int j = 0; j < 2 * kJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) T[i][j][e] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          uint32_t a[1][4];
-#pragma unroll
-          for (int i = 0; i < 1; ++i) ldsm4(block_rows<64>(tA, gr + 16 * i, 2 * kk, lane), a[i]);
-#pragma unroll
-          for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-              uint32_t b[4];
-              ldsm4t(block_rows<N>(tS + piece * kTileBytes<N>, 16 * kk, gc / 8 + 2 * j, lane), b);
-#pragma unroll
-              for (int i = 0; i < 1; ++i) {
-                mma16816(T[i][2 * j], a[i], b[0], b[1]);
-                mma16816(T[i][2 * j + 1], a[i], b[2], b[3]);
-              }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 1; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = gr + 16 * i + g + 8 * e;
-            const float f = side ? m.w[r] : m.gam[r];
-            float s = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 2 * kJ; ++j) {
-              uint32_t o;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o) : "r"(tile_at<N>(tO, r, gc / 8 + j) + q * 4));
-              float oa, ob;
-              bf2_get(o, oa, ob);
-              const float ta = f * T[i][j][2 * e], tb = f * T[i][j][2 * e + 1];
-              s = fmaf(oa, ta, fmaf(ob, tb, s));
-              if (side) {
-                aB[i][j][2 * e] += ta;
-                aB[i][j][2 * e + 1] += tb;
-              } else {
-                aC[i][j][2 * e] += ta;
-                aC[i][j][2 * e + 1] += tb;
-              }
-            }
-            if (side) qsum[i][e] += s;
-            else rsum[i][e] += s;
-          }
+      with_state(0, tY, sH, 2);
+      if (pt == 0) {
+        __syncthreads();  // Z has been read
+        fetch_third(adjoints, base + L::G3, h, 0);
+        copy_commit();
       }
-      // du = M^T dy + e^{c_n - c_j} B G^T, dx, x . du
+      with_state(1, tX, sG, 2);
+      // du = M^T dy + e^{c_n - c_j} B G^T and dx
       {
         float U[1][2][4], T[1][2][4];
 #pragma unroll
@@ -354,52 +383,52 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
             const float d = m.del[r], dt = m.dt[r];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              uint32_t xr, yr;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(xr) : "r"(tile_at<64>(tX, r, uc / 8 + j) + q * 4));
+              uint32_t yr;
               asm volatile("ld.shared.b32 %0, [%1];" : "=r"(yr) : "r"(tile_at<64>(tY, r, uc / 8 + j) + q * 4));
-              float xa, xb, ya, yb;
-              bf2_get(xr, xa, xb);
+              float ya, yb;
               bf2_get(yr, ya, yb);
               const float ua = fmaf(d, T[i][j][2 * e], U[i][j][2 * e]);
               const float ub = fmaf(d, T[i][j][2 * e + 1], U[i][j][2 * e + 1]);
-              xsum[i][e] = fmaf(xa, ua, fmaf(xb, ub, xsum[i][e]));
               if (r < n)
                 *reinterpret_cast<uint32_t *>(dx + ((row0 + r) * in.H + h) * P + pt * 64 + uc + 8 * j + 2 * q) =
                     bf2_set(fmaf(dt, ua, Dh * ya), fmaf(dt, ub, Dh * yb));
             }
           }
       }
+      copy_wait<0>();
+      __syncthreads();  // the third pieces are there
+      with_state(0, tY, base + L::H3, 1);
+      with_state(1, tX, base + L::G3, 1);
       // <G, H0>
-      for (int i = tid; i < 64 * N / 8; i += kGradThreads) {
-        const uint32_t at = tile_at<N>(0, i / (N / 8), i % (N / 8));
-        uint32_t a[4], b[4], c[4], d[4];
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(sH + at));
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]) : "r"(sH + kTileBytes<N> + at));
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(sG + at));
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(sG + kTileBytes<N> + at));
+      for (int i = tid; i < 64 * N / 4; i += kGradThreads) {  // four values of a row
+        const uint32_t at = (uint32_t)(i / (N / 4)) * kRowBytes<N> + (uint32_t)(i % (N / 4)) * 8;
+        float v[2][4] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p0, p1, l0, l1, g0, g1, k0, k1;
-          bf2_get(a[e], p0, p1);
-          bf2_get(b[e], l0, l1);
-          bf2_get(c[e], g0, g1);
-          bf2_get(d[e], k0, k1);
-          gh = fmaf(p0 + l0, g0 + k0, fmaf(p1 + l1, g1 + k1, gh));
-        }
+        for (int k = kPieces - 1; k >= 0; --k)
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const uint32_t from = k < 2 ? (side ? sG : sH) + k * kTileBytes<N> : base + (side ? L::G3 : L::H3);
+            uint32_t a, b;
+            asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(from + at));
+            float p[4];
+            bf2_get(a, p[0], p[1]);
+            bf2_get(b, p[2], p[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[side][e] += p[e];
+          }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gh = fmaf(v[0][e], v[1][e], gh);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 1; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = gr + 16 * i + g + 8 * e;
-        const float a = quad_sum(rsum[i][e]), b = quad_sum(qsum[i][e]), c = quad_sum(xsum[i][e]);
-        if (q == 0) {
-          rs.r[warp & 3][r] = a;
-          rs.q[warp & 3][r] = b;
-          rs.xdu[warp & 3][r] = c;
-        }
+    for (int e = 0; e < 2; ++e) {
+      const int r = gr + g + 8 * e;
+      const float a = quad_sum(rsum[e]), b = quad_sum(qsum[e]);
+      if (q == 0) {
+        rs.r[warp & 3][r] = a;
+        rs.q[warp & 3][r] = b;
       }
+    }
     gh = warp_sum(gh);
     if (lane == 0) rs.gh[warp] = gh;
     __syncthreads();  // every tile of this head has been read
@@ -414,11 +443,8 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
     if (tid < 256) {
       const int tt = tid >> 2, b = tid & 3;
       float s = 0.0f;
-      for (int c = 16 * b; c < min(16 * b + 16, tt); ++c) {
-        s += sZ[tt * 65 + c];
-        for (int k = tt / 16 + 1; k < 4; ++k) s += rs.zb[k][c];
-        s += (rs.q[0][c] + rs.q[1][c]) + (rs.q[2][c] + rs.q[3][c]);
-      }
+      for (int c = 16 * b; c < min(16 * b + 16, tt); ++c)
+        s = fmaf(m.dt[c], (rs.q[0][c] + rs.q[1][c]) + (rs.q[2][c] + rs.q[3][c]), s);
       for (int c = max(16 * b, tt); c < 16 * b + 16; ++c)
         s += (rs.r[0][c] + rs.r[1][c]) + (rs.r[2][c] + rs.r[3][c]);
       s = quad_sum(s);
@@ -426,7 +452,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < 16; ++w) v += rs.gh[w];
-        rs.l[tt] = fmaf(m.all, v, s);
+        rs.l[tt] = fmaf(m.all, v, s + rs.lz[tt]);
       }
     }
     __syncthreads();
@@ -437,7 +463,9 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       for (int k = 0; k < 2; ++k) {
         const int r = lane + 32 * k;
         if (r < n) {
-          const float x = (rs.xdu[0][r] + rs.xdu[1][r]) + (rs.xdu[2][r] + rs.xdu[3][r]);
+          // x . du: Z's column, and q
+          const float x = ((rs.zb[0][r] + rs.zb[1][r]) + (rs.zb[2][r] + rs.zb[3][r])) +
+                          ((rs.q[0][r] + rs.q[1][r]) + (rs.q[2][r] + rs.q[3][r]));
           const float d = fmaf(A, rs.l[r], x) * m.sig[r];
           draw[(row0 + r) * in.H + h] = __float2bfloat16_rn(d);
           dA = fmaf(m.dt[r], rs.l[r], dA);

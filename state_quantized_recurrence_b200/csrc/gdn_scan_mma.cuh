@@ -3,16 +3,29 @@
 //   M_ij = (C_i . B_j) e^{c_i - c_j} dt_j  (i >= j)
 //   y = M x + e^{c_i} C_i S_0 + D x,   S_n = e^{c_n} S_0 + sum_j B_j (w_j x_j)^T,
 //   w_j = e^{c_n - c_j} dt_j.
-// A CTA of four warps carries the state of one (sequence, head, 64 columns of
-// P) through a run of chunks.  The state stays in registers as the
-// accumulators of S^T (warp w: columns 16 w .. + 15 of P as rows, all N as
-// columns), a layout that is at once the B operand of C S_0, so the state
-// never passes through shared memory.
+// A CTA of eight warps carries the state of one (sequence, head, 64 columns
+// of P) through a run of chunks.  The state stays in registers as the
+// accumulators of S^T (warp w: columns 16 (w mod 4) .. + 15 of P as rows, half
+// w / 4 of N as columns), a layout that is at once the B operand of C S_0, so
+// the state never passes through shared memory; the two halves' parts of
+// C S_0 are exchanged instead.
 //
 // Precision: x, B, C are exact bf16 operands.  fp32 operands are split into
 // bf16 pieces: two for M and S_0 as they enter y (2^-17 relative, far under
 // y's own bf16 rounding), three for w x as it enters the state (2^-25: the
 // state stays an fp32 quantity).  Everything is accumulated in fp32.
+//
+// Why mma.sync: the products are small (64 x 64 x 128 and less, 3.3 million
+// multiply-adds a chunk at N = 128 with the pieces), and at such sizes
+// tcgen05 with both operands in shared memory was measured at 70 cycles for
+// M = 128, N = 64, K = 16, against 128 at the legacy rate of 1024
+// multiply-adds a clock; it would save the tensor pipe half its time but not
+// the splits, exponentials and copies, which are four fifths of the
+// instructions here, and would bring the state through TMEM and shared memory
+// every chunk.  Measured on 64 packed sequences (131 thousand tokens, 16
+// heads, P = 64): 0.78 ms, 6.6 thousand cycles a chunk and unit against 3.3
+// thousand of tensor pipe and 3.4 thousand of instruction issue; bound by how
+// little of the two overlaps with 16 warps an SM (128 registers each).
 #pragma once
 
 #include "gdn_scan_simt.cuh"
@@ -70,13 +83,6 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t 
   rest_of(a, b, mid);
   lo = bf2_set(a, b);
 }
-// v *= s
-__device__ __forceinline__ void scale4(float (&v)[4], float s) {
-  const uint64_t k = f2_pack(s, s);
-  f2_unpack(f2_mul(f2_pack(v[0], v[1]), k), v[0], v[1]);
-  f2_unpack(f2_mul(f2_pack(v[2], v[3]), k), v[2], v[3]);
-}
-
 // Tiles of 64 rows of COLS bf16 with 16 bytes behind each row: eight rows of
 // one 16-byte column lie in different banks, and an address is a lane's own
 // part plus a constant (exchanging column bits with the row's instead costs
@@ -192,8 +198,9 @@ __device__ __forceinline__ void decays_of(const RawSteps &raw, int n, float A, f
 enum Leave : int {
   kY = 0,      // y of every token and the last state
   kEnds = 1,   // the state that the run adds to zero, and its decay
-  kChunks = 2  // the state at every chunk's start (backwards: end), as bf16 pairs
+  kChunks = 2  // the state at every chunk's start (backwards: end), in bf16 pieces
 };
+constexpr int kPieces = 3;  // of such a state: together 2^-25 relative
 
 template <int N, int LEAVE>
 struct SweepSmem {
@@ -202,7 +209,7 @@ struct SweepSmem {
   static constexpr uint32_t M = X + 2 * kTileBytes<64>;
   static constexpr uint32_t E = M + (Y ? 2 * kTileBytes<64> : 0);    // halves of C S_0 on their way
   static constexpr uint32_t O = E + (Y ? 8 * 16 * 32 * 4 : 0);    // a chunk's state on its way out
-  static constexpr uint32_t D = O + (LEAVE == kChunks ? 2 * kTileBytes<N> : 0);
+  static constexpr uint32_t D = O + (LEAVE == kChunks ? kPieces * kTileBytes<N> : 0);
   static constexpr uint32_t bytes = D + 2 * sizeof(Decays);
 };
 constexpr int kSweepThreads = 256;
@@ -270,6 +277,11 @@ start_states_kernel(const int *__restrict__ cu, int n_seq, int T, int H, long lo
   else start_states<true>(cu, n_seq, T, H, np, last, seg_chunks, rev);
 }
 
+// Two barriers a chunk: the tiles of B and x are double, C's is filled again
+// as soon as M and C S_0 have been formed.  With four warps that hold all of
+// N (168 registers, three CTAs an SM) packed batches ran the same (0.75 ms),
+// one long sequence slower (0.11 ms against 0.08).
+//
 // REV: the adjoint G backwards over the chunks, G_0 = e^{c_n} G_n + sum_i
 // e^{c_i} C_i dy_i^T, with C in B's place, dy in x's and e^{c_i} in w's.
 template <int N, int LEAVE, bool REV>
@@ -354,7 +366,7 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
     RawSteps raw;
     if (warp == 7 && more) raw = raw_steps(in, row_of(cn), rows_in(cn), h);
     copy_wait<0>();
-    if (LEAVE == kChunks && tid < 128) sm100::bulk_wait_read_all();
+    if (LEAVE == kChunks && tid < 64 * kPieces) sm100::bulk_wait_read_all();
     __syncthreads();  // this chunk is there, the last one's B, x and M are free
     if (more) {
       fetch_tile<N, kSweepThreads>(sB0 + ((k + 1) & 1) * kTileBytes<N>, Bp + row_of(cn) * Bs, Bs, rows_in(cn), tid);
@@ -362,7 +374,7 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
       copy_commit();
     }
 
-    if constexpr (LEAVE == kChunks) {  // rows p of N bf16: hi, then lo
+    if constexpr (LEAVE == kChunks) {  // rows p of N bf16, piece by piece
       // Through shared memory and one bulk copy a row: the accumulators'
       // layout would store 16 bytes of each 32-byte sector (114 us against
       // 89 for both sweeps of 2 x 4096 tokens x 16 heads).
@@ -371,18 +383,19 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
       for (int i = 0; i < kT; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          uint32_t hi, lo;
-          split2(st[i][2 * e], st[i][2 * e + 1], hi, lo);
+          uint32_t u[kPieces];
+          split3(st[i][2 * e], st[i][2 * e + 1], u[0], u[1], u[2]);
           const uint32_t a = sO + (pw * 16 + g + 8 * e) * kRowBytes<N> + (n0 + 8 * i) * 2;
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(hi) : "memory");
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + kTileBytes<N>), "r"(lo) : "memory");
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + k * kTileBytes<N>), "r"(u[k]) : "memory");
         }
       sm100::fence_proxy_async();
       __syncthreads();
-      if (tid < 128) {
+      if (tid < 64 * kPieces) {
         const long long slot64 = in.cu ? t.seq + t.start / 64 + c : (long long)t.seq * chunks + c;
         const int piece = tid >> 6, p = tid & 63;
-        uint32_t *o = chunk_states + ((slot64 * in.H + h) * 2 + piece) * (np / 2) + (pt * 64 + p) * (long long)(N / 2);
+        uint32_t *o = chunk_states + ((slot64 * in.H + h) * kPieces + piece) * (np / 2) + (pt * 64 + p) * (long long)(N / 2);
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(o),
                      "r"(sO + piece * kTileBytes<N> + p * kRowBytes<N>), "r"(N * 2)
                      : "memory");
@@ -488,10 +501,30 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
       }
     }
 
-    // the state's decay, then both products that read x
+    // Both products that read x.  The sweeps of the gradient sum what the
+    // chunk adds to the state by itself: the tensor pipe truncates a sum at its
+    // own magnitude, and twelve of those a chunk at the state's cost a slowly
+    // forgetting one 1.5e-6 of its adjoint.  The forward sweep, whose states
+    // stay within 4e-7, has no registers for it (spills: 281 -> 349 us on 4 x
+    // 4096 tokens x 16 heads) and adds to the decayed state itself.
+    constexpr bool kApart = LEAVE != kY;
     const float all = m.all;
+    const uint64_t all2 = f2_pack(all, all);
+    float add[kApart ? kT : 1][4];
+    auto sum = [&](int i) -> float(&)[4] {
+      if constexpr (kApart) return add[i];
+      else return st[i];
+    };
 #pragma unroll
-    for (int i = 0; i < kT; ++i) scale4(st[i], all);
+    for (int i = 0; i < kT; ++i) {
+      if constexpr (kApart) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add[i][e] = 0.0f;
+      } else {
+        f2_unpack(f2_mul(f2_pack(st[i][0], st[i][1]), all2), st[i][0], st[i][1]);
+        f2_unpack(f2_mul(f2_pack(st[i][2], st[i][3]), all2), st[i][2], st[i][3]);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t x[4];  // (p, p + 8) x (j, j + 8) of x^T
@@ -527,19 +560,26 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
         ldsm4t(block_rows<N>(sB, 16 * j, nh * (N / 16) + 2 * i + 2, lane), b[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mma16816(st[2 * (i + e)], u0, b[e][0], b[e][1]);
-          mma16816(st[2 * (i + e) + 1], u0, b[e][2], b[e][3]);
+          mma16816(sum(2 * (i + e)), u0, b[e][0], b[e][1]);
+          mma16816(sum(2 * (i + e) + 1), u0, b[e][2], b[e][3]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mma16816(st[2 * (i + e)], u1, b[e][0], b[e][1]);
-          mma16816(st[2 * (i + e) + 1], u1, b[e][2], b[e][3]);
+          mma16816(sum(2 * (i + e)), u1, b[e][0], b[e][1]);
+          mma16816(sum(2 * (i + e) + 1), u1, b[e][2], b[e][3]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mma16816(st[2 * (i + e)], u2, b[e][0], b[e][1]);
-          mma16816(st[2 * (i + e) + 1], u2, b[e][2], b[e][3]);
+          mma16816(sum(2 * (i + e)), u2, b[e][0], b[e][1]);
+          mma16816(sum(2 * (i + e) + 1), u2, b[e][2], b[e][3]);
         }
+      }
+    }
+    if constexpr (kApart) {
+#pragma unroll
+      for (int i = 0; i < kT; ++i) {
+        f2_unpack(f2_fma(f2_pack(st[i][0], st[i][1]), all2, f2_pack(add[i][0], add[i][1])), st[i][0], st[i][1]);
+        f2_unpack(f2_fma(f2_pack(st[i][2], st[i][3]), all2, f2_pack(add[i][2], add[i][3])), st[i][2], st[i][3]);
       }
     }
     if (LEAVE == kEnds) run_decay *= all;
@@ -566,7 +606,7 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
     if (more && LEAVE != kY && warp == 7) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
   }
 
-  if (LEAVE == kChunks && tid < 128) sm100::bulk_wait_all();
+  if (LEAVE == kChunks && tid < 64 * kPieces) sm100::bulk_wait_all();
   float *dst = nullptr;
   if (LEAVE == kEnds) {
     dst = ends.state + (slot * in.H + h) * np + p0;

@@ -37,8 +37,8 @@ __device__ __forceinline__ float softplus(float x) {
 //   kAdjoint   backwards, with C and dy in the places of B and u:
 //              G <- a_t (G + C_t dy_t^T); the adjoint of the state at the end
 //              of every chunk -> dump[slot], the last one -> dstate_in
-// Bound by the instruction stream: 3 fp32 operations and a quarter of a
-// shared-memory load for each state element and token.
+// Bound by the instruction stream: 4 fp32 operations and half a shared-memory
+// load for each state element and token.
 enum Sweep : int { kForward = 0, kStates = 1, kAdjoint = 2 };
 constexpr int kTok = 16;  // tokens staged at a time
 
@@ -48,7 +48,7 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
                                       float *out_state, float *__restrict__ dump, unsigned *err) {
   constexpr int R = N / 4;
   __shared__ __align__(16) float sb[kTok][N], sc[kTok][N], su[kTok][64], sy[4][kTok][64];
-  __shared__ float sa[kTok], sdt[kTok];
+  __shared__ float sa[kTok], sal[kTok], sdt[kTok];
   const int tid = threadIdx.x, p = tid & 63, q = tid >> 6;
   const int npt = in.P / 64;
   const int pt = blockIdx.x % npt, h = blockIdx.x / npt % in.H;
@@ -86,7 +86,11 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
     if (tid < n) {
       const float dt = softplus(to_f32(in.raw[(t0 + b0 + tid) * in.rs + h]) + bias);
       sdt[tid] = dt;
-      sa[tid] = expf(dt * A);
+      // The decay as two floats: its rounding alone, multiplied up over a few
+      // hundred tokens, costs a slowly forgetting state 1e-6.
+      const double a = exp((double)dt * (double)A);
+      sa[tid] = (float)a;
+      sal[tid] = (float)(a - (double)sa[tid]);
     }
     for (int i = tid; i < n * 64; i += 256) {
       const long long row = t0 + b0 + i / 64;
@@ -101,14 +105,16 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
 #pragma unroll
           for (int i = 0; i < R; ++i) d[(long long)(q * R + i) * in.P] = st[i];
         }
-        const float a = sa[t], u = su[t][p];
+        const float a = sa[t], al = sal[t], u = su[t][p];
 #pragma unroll
         for (int i = 0; i < R; i += 4) {
           const float4 c = *reinterpret_cast<const float4 *>(&sc[t][q * R + i]);
-          st[i] = a * fmaf(c.x, u, st[i]);
-          st[i + 1] = a * fmaf(c.y, u, st[i + 1]);
-          st[i + 2] = a * fmaf(c.z, u, st[i + 2]);
-          st[i + 3] = a * fmaf(c.w, u, st[i + 3]);
+          const float v0 = fmaf(c.x, u, st[i]), v1 = fmaf(c.y, u, st[i + 1]);
+          const float v2 = fmaf(c.z, u, st[i + 2]), v3 = fmaf(c.w, u, st[i + 3]);
+          st[i] = fmaf(a, v0, al * v0);
+          st[i + 1] = fmaf(a, v1, al * v1);
+          st[i + 2] = fmaf(a, v2, al * v2);
+          st[i + 3] = fmaf(a, v3, al * v3);
         }
       }
     } else {
@@ -118,15 +124,15 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
 #pragma unroll
           for (int i = 0; i < R; ++i) d[(long long)(q * R + i) * in.P] = st[i];
         }
-        const float a = sa[t], u = sdt[t] * su[t][p];
+        const float a = sa[t], al = sal[t], u = sdt[t] * su[t][p];
         float acc = 0.0f;
 #pragma unroll
         for (int i = 0; i < R; i += 4) {
           const float4 b = *reinterpret_cast<const float4 *>(&sb[t][q * R + i]);
-          st[i] = fmaf(a, st[i], b.x * u);
-          st[i + 1] = fmaf(a, st[i + 1], b.y * u);
-          st[i + 2] = fmaf(a, st[i + 2], b.z * u);
-          st[i + 3] = fmaf(a, st[i + 3], b.w * u);
+          st[i] = fmaf(a, st[i], fmaf(al, st[i], b.x * u));
+          st[i + 1] = fmaf(a, st[i + 1], fmaf(al, st[i + 1], b.y * u));
+          st[i + 2] = fmaf(a, st[i + 2], fmaf(al, st[i + 2], b.z * u));
+          st[i + 3] = fmaf(a, st[i + 3], fmaf(al, st[i + 3], b.w * u));
           if constexpr (MODE == kForward) {
             const float4 c = *reinterpret_cast<const float4 *>(&sc[t][q * R + i]);
             acc = fmaf(c.x, st[i], acc);
