@@ -1,6 +1,10 @@
 // Gradient of the scan's chunks for bf16 inputs on the tensor cores: the
-// algebra of chunk_grad_kernel with mma.sync products of bf16 pieces (pairs
-// for M, W, the states and the adjoints: 2^-17 relative).
+// algebra of chunk_grad_kernel with mma.sync products of bf16 pieces.  What is
+// rounded to bf16 in the end (dx, dB, dC, the step's gradient) takes pairs
+// (2^-17 relative) for M and W; what dA and ddt_bias add up over all tokens is
+// kept to fp32's own rounding: Z stays fp32, x_t . du_t is taken from Z's
+// columns instead of du, and the states and adjoints come in three pieces
+// (with two, dA was up to 8e-6 off; the third costs 45 us of the 232 below).
 //
 // A CTA of sixteen warps takes one chunk and a range of one group's heads.
 // S = C B^T is formed once; dB and dC are summed over the heads in the
@@ -8,14 +12,11 @@
 // heads split over several CTAs, their fp32 parts are added afterwards in
 // order).
 //
-// 2 x 4096 tokens x 16 heads, N = 128, P = 64: 188 us, 22 thousand cycles a
-// head and chunk, of which the tensor pipe is busy 5.4 (24 %), the shared
-// memory pipe 49 %; the rest is the latency of four dependent stages between
-// barriers.  Eight warps with twice the tile ran the same (181 us).
-//
-// dA and ddt_bias add up e^{c_i} C_i . H0 dy_i, dt_j e^{..} B_j . G x_j and
-// <G, H0>, whose states enter as bf16 pairs: a few 1e-6 relative.  The part
-// inside a chunk (Z) is fp32 throughout.
+// 2 x 4096 tokens x 16 heads, N = 128, P = 64: 232 us, 27 thousand cycles a
+// head and chunk for 6.5 of tensor pipe and about 12 of shared-memory pipe
+// (its two-piece form: 24 % and 49 % busy); the rest is the latency of
+// dependent stages between seven barriers.  Eight warps with twice the tile
+// ran the same in the two-piece form (181 us against 188).
 #pragma once
 
 #include "gdn_scan_mma.cuh"
