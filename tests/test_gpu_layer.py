@@ -247,3 +247,70 @@ def test_given_stream(cuda_lib):
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
         del junk
+
+
+def _far_apart(rows, width, stride, dtype, gen):
+    """[1, rows, width] whose tokens lie `stride` elements apart: the last
+    one's offset passes 2^31 elements (and 32 bits of bytes)."""
+    base = torch.empty((rows - 1) * stride + width, dtype=dtype, device="cuda")
+    x = base.as_strided((1, rows, width), (rows * stride, stride, 1))
+    x.copy_(torch.randn(1, rows, width, generator=gen))
+    return x
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    g = torch.Generator().manual_seed(8)
+    T, stride = 70, 1 << 25
+    x = _far_apart(T, 256, stride, BF16, g)
+    assert (T - 1) * stride > 1 << 31
+    near = x.contiguous()
+    w = torch.randn(256, W, generator=g).cuda()
+    dy = torch.randn(1, T, 256, generator=g).to(BF16).cuda()
+    for far, close in zip(cuda_lib.gdn_conv_prefill(x, w) + cuda_lib.gdn_conv_backward(x, w, dy),
+                          cuda_lib.gdn_conv_prefill(near, w)
+                          + cuda_lib.gdn_conv_backward(near, w, dy)):
+        assert torch.equal(far, close)
+    one = torch.ones(256, device="cuda")
+    assert torch.equal(cuda_lib.gdn_norm(x, one)[0], cuda_lib.gdn_norm(near, one)[0])
+    for far, close in zip(cuda_lib.gdn_norm_backward(x, one, dy)[:2],
+                          cuda_lib.gdn_norm_backward(near, one, dy)[:2]):
+        assert torch.equal(far, close)
+    A = -torch.rand(2, generator=g).cuda() - 0.5
+    dt = torch.randn(1, T, 2, generator=g).to(BF16).cuda()
+
+    def scan(t, d):
+        a = (t[..., :128].unflatten(-1, (2, 64)), d, A, t[..., 128:192].unflatten(-1, (1, 64)),
+             t[..., 192:].unflatten(-1, (1, 64)))
+        return cuda_lib.gdn_scan_prefill(*a) + cuda_lib.gdn_scan_backward(
+            *a, dy[..., :128].unflatten(-1, (2, 64)).contiguous())
+
+    for far, close in zip(scan(x, dt), scan(near, dt)):
+        assert torch.equal(far, close)
+
+
+def test_packed_call_replayed_with_other_lengths(cuda_lib):
+    """A captured packed call reads cu_seqlens when it is replayed."""
+    L = Layer(BF16)
+    g = torch.Generator().manual_seed(9)
+    T = 300
+    xbc = torch.randn(1, T, XBC, generator=g).to(BF16).cuda()
+    dt = torch.randn(1, T, H, generator=g).to(BF16).cuda()
+    cus = [torch.tensor(c, dtype=torch.int32, device="cuda")
+           for c in ([0, 100, 200, 300], [0, 0, 299, 300], [0, 300, 300, 300])]
+
+    def run(cu):
+        c, cs = cuda_lib.gdn_conv_prefill(xbc, L.conv_w, L.conv_b, None, cu)
+        u, B, C = L.xbc(c)
+        return (c, cs) + cuda_lib.gdn_scan_prefill(u, dt, L.A, B, C, D=L.D, cu_seqlens=cu)
+
+    want = [run(cu) for cu in cus]
+    cu = cus[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(cu)
+    for c, w in zip(cus, want):
+        cu.copy_(c)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
+    cuda_lib.check_last_error()
