@@ -94,52 +94,59 @@ Plan plan(int n_seq, int T, int H, int P, int N, bool packed) {
 unsigned run_blocks(const Call &c, const Plan &p) { return (unsigned)(p.slots * c.H * (c.P / 64)); }
 
 // What the runs add, then what they start from; rev.state: backwards too.
-template <int N>
-gdn_status run_starts(const Call &c, const Plan &p, const __nv_bfloat16 *dy, const float *dstate_out, Ends fwd,
-                      Ends rev, unsigned *err, cudaStream_t st) {
-  const In<__nv_bfloat16> in = typed<__nv_bfloat16>(c);
-  constexpr int smem = (int)SweepSmem<N, kEnds>::bytes;
-  const unsigned both = rev.state ? 2 : 1;
-  static std::atomic<uint64_t> done{0};
-  if (!allow_smem(ends_mma_kernel<N>, smem, done)) return GDN_ERR_CUDA;
-  ends_mma_kernel<N><<<dim3(run_blocks(c, p), both), kSweepThreads, smem, st>>>(in, dy, p.seg_chunks, fwd, rev, err);
+template <typename T, int N>
+gdn_status run_starts(const Call &c, const Plan &p, const T *dy, const float *dstate_out, Ends fwd, Ends rev,
+                      unsigned *err, cudaStream_t st) {
+  const In<T> in = typed<T>(c);
+  const dim3 grid(run_blocks(c, p), rev.state ? 2 : 1);
+  if constexpr (sizeof(T) == 2) {
+    constexpr int smem = (int)SweepSmem<N, kEnds>::bytes;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(ends_mma_kernel<N>, smem, done)) return GDN_ERR_CUDA;
+    ends_mma_kernel<N><<<grid, kSweepThreads, smem, st>>>(in, dy, p.seg_chunks, fwd, rev, err);
+  } else {
+    adds_kernel<T, N><<<grid, 256, 0, st>>>(in, dy, p.seg_chunks, fwd, rev, err);
+  }
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   const long long np = (long long)c.N * c.P;
-  start_states_kernel<<<dim3((unsigned)(c.n_seq * c.H * (np / 1024)), both), 256, 0, st>>>(
+  start_states_kernel<<<dim3((unsigned)(c.n_seq * c.H * (np / 1024)), grid.y), 256, 0, st>>>(
       c.cu, c.n_seq, c.T, c.H, np, c.state_in, dstate_out, p.seg_chunks, fwd, rev);
   return launched();
 }
+Ends ends_at(char *ws, size_t state, size_t decay) {
+  return Ends{reinterpret_cast<float *>(ws + state), reinterpret_cast<float *>(ws + decay)};
+}
 
-template <int N>
-gdn_status prefill_mma(const Call &c, char *ws, void *y, float *state_out, unsigned *err, cudaStream_t st) {
-  const In<__nv_bfloat16> in = typed<__nv_bfloat16>(c);
+template <typename T, int N>
+gdn_status prefill_typed(const Call &c, char *ws, void *y, float *state_out, unsigned *err, cudaStream_t st) {
+  const In<T> in = typed<T>(c);
   const Plan p = plan(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr);
   Ends ends{nullptr, nullptr};
   if (p.split) {
-    ends = Ends{reinterpret_cast<float *>(ws + p.state), reinterpret_cast<float *>(ws + p.decay)};
-    const gdn_status s = run_starts<N>(c, p, nullptr, nullptr, ends, Ends{nullptr, nullptr}, err, st);
+    ends = ends_at(ws, p.state, p.decay);
+    const gdn_status s = run_starts<T, N>(c, p, nullptr, nullptr, ends, Ends{nullptr, nullptr}, err, st);
     if (s != GDN_OK) return s;
   }
-  constexpr int smem = (int)SweepSmem<N, kY>::bytes;
-  static std::atomic<uint64_t> done{0};
-  if (!allow_smem(scan_mma_kernel<N>, smem, done)) return GDN_ERR_CUDA;
-  scan_mma_kernel<N><<<run_blocks(c, p), kSweepThreads, smem, st>>>(
-      in, p.seg_chunks, ends, static_cast<__nv_bfloat16 *>(y), state_out, err);
+  if constexpr (sizeof(T) == 2) {
+    constexpr int smem = (int)SweepSmem<N, kY>::bytes;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(scan_mma_kernel<N>, smem, done)) return GDN_ERR_CUDA;
+    scan_mma_kernel<N><<<run_blocks(c, p), kSweepThreads, smem, st>>>(in, p.seg_chunks, ends,
+                                                                      static_cast<T *>(y), state_out, err);
+  } else {
+    forward_kernel<T, N><<<run_blocks(c, p), 256, 0, st>>>(in, p.seg_chunks, ends, static_cast<T *>(y),
+                                                           state_out, err);
+  }
   return launched();
 }
 
 gdn_status prefill(const Call &c, gdn_dtype dt, char *ws, void *y, float *state_out, unsigned *err,
                    cudaStream_t st) {
   if (dt == GDN_DTYPE_BF16)
-    return c.N == 128 ? prefill_mma<128>(c, ws, y, state_out, err, st)
-                      : prefill_mma<64>(c, ws, y, state_out, err, st);
-  const In<float> in = typed<float>(c);
-  float *yo = static_cast<float *>(y);
-  if (c.N == 128)
-    forward_kernel<float, 128><<<units(c), 256, 0, st>>>(in, yo, state_out, err);
-  else
-    forward_kernel<float, 64><<<units(c), 256, 0, st>>>(in, yo, state_out, err);
-  return launched();
+    return c.N == 128 ? prefill_typed<__nv_bfloat16, 128>(c, ws, y, state_out, err, st)
+                      : prefill_typed<__nv_bfloat16, 64>(c, ws, y, state_out, err, st);
+  return c.N == 128 ? prefill_typed<float, 128>(c, ws, y, state_out, err, st)
+                    : prefill_typed<float, 64>(c, ws, y, state_out, err, st);
 }
 
 template <typename T>
@@ -154,7 +161,7 @@ gdn_status decode(const Call &c, float *state, void *y, cudaStream_t st) {
 // every chunk's start and its adjoint at every chunk's end (fp32, or three
 // bf16 pieces), dB and dC of every head (fp32) or of every share of a group's
 // heads (bf16, where there are several), the heads' parameters' parts of
-// every chunk, and for bf16 what runs of chunks hand over.
+// every chunk, and what runs of chunks hand over.
 struct Workspace {
   Plan runs;
   long long slots, rows;
@@ -193,15 +200,13 @@ Workspace workspace(int n_seq, int T, int H, int P, int G, int N, gdn_dtype dt, 
   w.dC = w.dB + sums;
   w.part = w.dC + sums;
   w.bytes = w.part + (size_t)w.slots * H * 16;
-  if (mma) {
-    w.runs = plan(n_seq, T, H, P, N, packed);
-    if (w.runs.split) {
-      w.fwd = w.bytes;
-      w.fwd_decay = w.fwd + w.runs.decay;
-      w.rev = w.fwd + w.runs.bytes;
-      w.rev_decay = w.rev + w.runs.decay;
-      w.bytes = w.rev + w.runs.bytes;
-    }
+  w.runs = plan(n_seq, T, H, P, N, packed);
+  if (w.runs.split) {
+    w.fwd = w.bytes;
+    w.fwd_decay = w.fwd + w.runs.decay;
+    w.rev = w.fwd + w.runs.bytes;
+    w.rev_decay = w.rev + w.runs.decay;
+    w.bytes = w.rev + w.runs.bytes;
   }
   return w;
 }
@@ -236,9 +241,16 @@ gdn_status backward_f32(const Call &c, const Grads &g, char *ws, unsigned *err, 
   float *states = reinterpret_cast<float *>(ws + w.states);
   float *adjoints = reinterpret_cast<float *>(ws + w.adjoints);
   const float *dy = static_cast<const float *>(g.dy);
-  boundaries_kernel<float, N><<<dim3(units(c), 2), 256, 0, st>>>(in, dy, g.dstate_out, states, adjoints,
-                                                                 g.dstate_in, err);
-  if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+  Ends fwd{nullptr, nullptr}, rev{nullptr, nullptr};
+  gdn_status s;
+  if (w.runs.split) {
+    fwd = ends_at(ws, w.fwd, w.fwd_decay);
+    rev = ends_at(ws, w.rev, w.rev_decay);
+    if ((s = run_starts<float, N>(c, w.runs, dy, g.dstate_out, fwd, rev, err, st)) != GDN_OK) return s;
+  }
+  boundaries_kernel<float, N><<<dim3(run_blocks(c, w.runs), 2), 256, 0, st>>>(
+      in, dy, g.dstate_out, w.runs.seg_chunks, fwd, rev, states, adjoints, g.dstate_in, err);
+  if ((s = launched()) != GDN_OK) return s;
   auto kern = chunk_grad_kernel<float, N, P>;
   constexpr size_t smem = ChunkLayout<N, P>::bytes;
   static std::atomic<uint64_t> done{0};
@@ -261,9 +273,9 @@ gdn_status backward_mma(const Call &c, const Grads &g, char *ws, unsigned *err, 
   uint32_t *adjoints = reinterpret_cast<uint32_t *>(ws + w.adjoints);
   gdn_status s;
   if (w.runs.split) {
-    fwd = Ends{reinterpret_cast<float *>(ws + w.fwd), reinterpret_cast<float *>(ws + w.fwd_decay)};
-    rev = Ends{reinterpret_cast<float *>(ws + w.rev), reinterpret_cast<float *>(ws + w.rev_decay)};
-    if ((s = run_starts<N>(c, w.runs, dy, g.dstate_out, fwd, rev, err, st)) != GDN_OK) return s;
+    fwd = ends_at(ws, w.fwd, w.fwd_decay);
+    rev = ends_at(ws, w.rev, w.rev_decay);
+    if ((s = run_starts<T, N>(c, w.runs, dy, g.dstate_out, fwd, rev, err, st)) != GDN_OK) return s;
   }
   constexpr int sweep_smem = (int)SweepSmem<N, kChunks>::bytes;
   static std::atomic<uint64_t> sweeps_done{0}, chunks_done{0};
@@ -302,7 +314,7 @@ size_t gdn_scan_prefill_workspace_bytes(int n_seq, int T, int H, int P, int G, i
                                         gdn_dtype dtype, int packed) {
   const scan::Call c{nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, nullptr, nullptr, nullptr,
                      nullptr, nullptr, 0, T, H, P, G, N};
-  if (n_seq <= 0 || dtype != GDN_DTYPE_BF16 || scan::check(c, dtype, false) != GDN_OK) return 0;
+  if (n_seq <= 0 || scan::check(c, dtype, false) != GDN_OK) return 0;
   return scan::plan(n_seq, T, H, P, N, packed != 0).bytes;
 }
 

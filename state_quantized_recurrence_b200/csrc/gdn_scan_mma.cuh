@@ -214,69 +214,6 @@ struct SweepSmem {
 };
 constexpr int kSweepThreads = 256;
 
-struct Ends {           // of the runs, where sequences are cut into several
-  float *state;         // [run slot][H][N][P]; NULL: one run a sequence
-  float *decay;         // [run slot][H]
-};
-
-// From what each run adds to zero (kEnds) to the state that each run starts
-// from, in place: run k starts from decay_{k-1} start_{k-1} + added_{k-1}.
-// A thread follows four state elements through the runs of a sequence.
-// Bound by latency; it keeps every run from adding up all that went before
-// it.
-template <bool REV>
-__device__ __forceinline__ void start_states(const int *__restrict__ cu, int n_seq, int T, int H, long long np,
-                                             const float *__restrict__ first, int seg_chunks, Ends ends) {
-  const int parts = (int)(np / 1024);
-  const int part = blockIdx.x % parts, h = blockIdx.x / parts % H;
-  const long long s = blockIdx.x / parts / H;
-  const long long L = seg_chunks * 64LL;
-  long long len = T, slot;
-  if (cu) {
-    if (!seq_ok(cu, n_seq, (int)s, T)) return;
-    len = cu[s + 1] - cu[s];
-    slot = s + cu[s] / L;
-  } else {
-    slot = s * (T > 0 ? (T + L - 1) / L : 1);
-  }
-  const int segs = (int)max(1LL, (len + L - 1) / L);
-  const long long at = part * 1024 + threadIdx.x * 4;
-  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (first) run = *reinterpret_cast<const float4 *>(first + (s * H + h) * np + at);
-  constexpr int kAhead = 8;  // runs loaded before the first is needed
-  for (int k0 = 0; k0 < segs; k0 += kAhead) {
-    float4 add[kAhead];
-    float d[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int k = k0 + u;
-      if (k >= segs - 1) continue;  // the last run adds to nobody
-      const long long w = slot + (REV ? segs - 1 - k : k);
-      add[u] = *reinterpret_cast<const float4 *>(ends.state + (w * H + h) * np + at);
-      d[u] = ends.decay[w * H + h];
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int k = k0 + u;
-      if (k >= segs) break;
-      const long long w = slot + (REV ? segs - 1 - k : k);
-      *reinterpret_cast<float4 *>(ends.state + (w * H + h) * np + at) = run;
-      if (k == segs - 1) break;
-      run.x = fmaf(d[u], run.x, add[u].x);
-      run.y = fmaf(d[u], run.y, add[u].y);
-      run.z = fmaf(d[u], run.z, add[u].z);
-      run.w = fmaf(d[u], run.w, add[u].w);
-    }
-  }
-}
-// blockIdx.y = 1 (where there are two): the adjoints, from the last run on.
-__global__ void __launch_bounds__(256)
-start_states_kernel(const int *__restrict__ cu, int n_seq, int T, int H, long long np, const float *first,
-                    const float *last, int seg_chunks, Ends fwd, Ends rev) {
-  if (blockIdx.y == 0) start_states<false>(cu, n_seq, T, H, np, first, seg_chunks, fwd);
-  else start_states<true>(cu, n_seq, T, H, np, last, seg_chunks, rev);
-}
-
 // Two barriers a chunk: the tiles of B and x are double, C's is filled again
 // as soon as M and C S_0 have been formed.  With four warps that hold all of
 // N (168 registers, three CTAs an SM) packed batches ran the same (0.75 ms),

@@ -30,58 +30,125 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
-// Sweep of one (sequence, head, 64-column tile of P) by 256 threads: thread
-// (p, q) holds rows q N/4 .. of column p.
+struct Ends {           // of the runs, where sequences are cut into several
+  float *state;         // [run slot][H][N][P]; NULL: one run a sequence
+  float *decay;         // [run slot][H]
+};
+
+// From what each run adds to zero (kEnds) to the state that each run starts
+// from, in place: run k starts from decay_{k-1} start_{k-1} + added_{k-1}.
+// A thread follows four state elements through the runs of a sequence.
+// Bound by latency; it keeps every run from adding up all that went before
+// it.
+template <bool REV>
+__device__ __forceinline__ void start_states(const int *__restrict__ cu, int n_seq, int T, int H, long long np,
+                                             const float *__restrict__ first, int seg_chunks, Ends ends) {
+  const int parts = (int)(np / 1024);
+  const int part = blockIdx.x % parts, h = blockIdx.x / parts % H;
+  const long long s = blockIdx.x / parts / H;
+  const long long L = seg_chunks * 64LL;
+  long long len = T, slot;
+  if (cu) {
+    if (!seq_ok(cu, n_seq, (int)s, T)) return;
+    len = cu[s + 1] - cu[s];
+    slot = s + cu[s] / L;
+  } else {
+    slot = s * (T > 0 ? (T + L - 1) / L : 1);
+  }
+  const int segs = (int)max(1LL, (len + L - 1) / L);
+  const long long at = part * 1024 + threadIdx.x * 4;
+  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (first) run = *reinterpret_cast<const float4 *>(first + (s * H + h) * np + at);
+  constexpr int kAhead = 8;  // runs loaded before the first is needed
+  for (int k0 = 0; k0 < segs; k0 += kAhead) {
+    float4 add[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u;
+      if (k >= segs - 1) continue;  // the last run adds to nobody
+      const long long w = slot + (REV ? segs - 1 - k : k);
+      add[u] = *reinterpret_cast<const float4 *>(ends.state + (w * H + h) * np + at);
+      d[u] = ends.decay[w * H + h];
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u;
+      if (k >= segs) break;
+      const long long w = slot + (REV ? segs - 1 - k : k);
+      *reinterpret_cast<float4 *>(ends.state + (w * H + h) * np + at) = run;
+      if (k == segs - 1) break;
+      run.x = fmaf(d[u], run.x, add[u].x);
+      run.y = fmaf(d[u], run.y, add[u].y);
+      run.z = fmaf(d[u], run.z, add[u].z);
+      run.w = fmaf(d[u], run.w, add[u].w);
+    }
+  }
+}
+// blockIdx.y = 1 (where there are two): the adjoints, from the last run on.
+__global__ void __launch_bounds__(256)
+start_states_kernel(const int *__restrict__ cu, int n_seq, int T, int H, long long np, const float *first,
+                    const float *last, int seg_chunks, Ends fwd, Ends rev) {
+  if (blockIdx.y == 0) start_states<false>(cu, n_seq, T, H, np, first, seg_chunks, fwd);
+  else start_states<true>(cu, n_seq, T, H, np, last, seg_chunks, rev);
+}
+
+// Sweep over one run of chunks of one (sequence, head, 64-column tile of P)
+// by 256 threads: thread (p, q) holds rows q N/4 .. of column p.
 //   kForward   y and the last state
 //   kStates    the state at the start of every chunk -> dump[slot]
 //   kAdjoint   backwards, with C and dy in the places of B and u:
 //              G <- a_t (G + C_t dy_t^T); the adjoint of the state at the end
-//              of every chunk -> dump[slot], the last one -> dstate_in
+//              of every chunk -> dump[slot], the last one -> out_state
+//   kAdds, kAddsBack   what the run adds to a zero state -> ends
 // Bound by the instruction stream: 4 fp32 operations and half a shared-memory
 // load for each state element and token.
-enum Sweep : int { kForward = 0, kStates = 1, kAdjoint = 2 };
+enum Sweep : int { kForward = 0, kStates = 1, kAdjoint = 2, kAdds = 3, kAddsBack = 4 };
 constexpr int kTok = 16;  // tokens staged at a time
 
 template <typename T, int N, int MODE>
-__device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
-                                      const float *__restrict__ last, T *__restrict__ y,
-                                      float *out_state, float *__restrict__ dump, unsigned *err) {
+__device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy, const float *first,
+                                      int seg_chunks, Ends ends, T *__restrict__ y, float *out_state,
+                                      float *__restrict__ dump, unsigned *err) {
   constexpr int R = N / 4;
+  constexpr bool kBack = MODE == kAdjoint || MODE == kAddsBack, kAdd = MODE == kAdds || MODE == kAddsBack;
   __shared__ __align__(16) float sb[kTok][N], sc[kTok][N], su[kTok][64], sy[4][kTok][64];
   __shared__ float sa[kTok], sal[kTok], sdt[kTok];
   const int tid = threadIdx.x, p = tid & 63, q = tid >> 6;
   const int npt = in.P / 64;
   const int pt = blockIdx.x % npt, h = blockIdx.x / npt % in.H;
-  const long long s = blockIdx.x / npt / in.H;
+  long long slot = blockIdx.x / npt / in.H;
   const int g = h / (in.H / in.G);
-  long long t0 = s * in.T_, len = in.T_, slot0;
-  if (in.cu) {
-    if (!seq_ok(in.cu, in.n_seq, (int)s, in.T_)) {
-      if (tid == 0) atomicOr(err, kErrBadSeqlens);
-      return;
-    }
-    t0 = in.cu[s];
-    len = in.cu[s + 1] - t0;
-    slot0 = s + t0 / kChunk;
-  } else {
-    slot0 = s * (in.T_ > 0 ? (in.T_ + kChunk - 1) / kChunk : 1);
-  }
+  if (in.cu && blockIdx.x == 0) check_seqlens(in.cu, in.n_seq, in.T_, err);
+  // packed sequences that are not cut into runs: the longest first
+  if (in.cu && seg_chunks * 64LL >= in.T_ && in.n_seq <= 256 && slot < in.n_seq)
+    slot = seq_of_rank(in.cu, in.n_seq, (int)slot);
+  const Tile tile = find_tile(in.cu, in.n_seq, in.T_, seg_chunks * kChunk, slot);
+  if (tile.seq < 0) return;
+  const long long t0 = tile.start, len = tile.len, s = tile.seq, L = (long long)seg_chunks * kChunk;
+  const long long segs = max(1LL, (len + L - 1) / L);
+  const bool last_run = kBack ? tile.tile == 0 : tile.tile == segs - 1;
+  if (kAdd && last_run) return;  // nobody follows
+  const long long slot0 = in.cu ? s + t0 / kChunk : s * (len > 0 ? (len + kChunk - 1) / kChunk : 1);
+  const long long from = tile.tile * L, to = min(len, from + L);
   const float A = in.A[h], D = in.D ? in.D[h] : 0.0f, bias = in.bias ? in.bias[h] : 0.0f;
-  const long long at = (s * in.H + h) * (long long)N * in.P + pt * 64 + p;
+  const long long np = (long long)N * in.P, mine = pt * 64 + p;
+  const long long at = (s * in.H + h) * np + mine, at_run = (slot * in.H + h) * np + mine;
   float st[R];
-  const float *first = MODE == kAdjoint ? last : in.state_in;
+  const float *src = kAdd ? nullptr : ends.state ? ends.state + at_run : first ? first + at : nullptr;
 #pragma unroll
-  for (int i = 0; i < R; ++i) st[i] = first ? first[at + (long long)(q * R + i) * in.P] : 0.0f;
+  for (int i = 0; i < R; ++i) st[i] = src ? src[(long long)(q * R + i) * in.P] : 0.0f;
+  double decay = 0.0;  // log of the run's
 
-  const long long tiles = (len + kTok - 1) / kTok;
+  const long long tiles = (to - from + kTok - 1) / kTok;
   for (long long k = 0; k < tiles; ++k) {
-    const long long b0 = (MODE == kAdjoint ? tiles - 1 - k : k) * kTok;
-    const int n = (int)min((long long)kTok, len - b0);
+    const long long b0 = from + (kBack ? tiles - 1 - k : k) * kTok;
+    const int n = (int)min((long long)kTok, to - b0);
     __syncthreads();
     for (int i = tid; i < n * N; i += 256) {
       const long long row = t0 + b0 + i / N;
-      if (MODE != kAdjoint) sb[i / N][i % N] = to_f32(in.B[row * in.bs + g * N + i % N]);
-      if (MODE != kStates) sc[i / N][i % N] = to_f32(in.C[row * in.cs + g * N + i % N]);
+      if (!kBack) sb[i / N][i % N] = to_f32(in.B[row * in.bs + g * N + i % N]);
+      if (kBack || MODE == kForward) sc[i / N][i % N] = to_f32(in.C[row * in.cs + g * N + i % N]);
     }
     if (tid < n) {
       const float dt = softplus(to_f32(in.raw[(t0 + b0 + tid) * in.rs + h]) + bias);
@@ -89,18 +156,19 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
       // The decay as two floats: its rounding alone, multiplied up over a few
       // hundred tokens, costs a slowly forgetting state 1e-6.
       const double a = exp((double)dt * (double)A);
+      if (kAdd) decay += (double)dt * (double)A;
       sa[tid] = (float)a;
       sal[tid] = (float)(a - (double)sa[tid]);
     }
     for (int i = tid; i < n * 64; i += 256) {
       const long long row = t0 + b0 + i / 64;
       const long long c = (long long)h * in.P + pt * 64 + i % 64;
-      su[i / 64][i % 64] = to_f32(MODE == kAdjoint ? dy[row * in.H * in.P + c] : in.x[row * in.xs + c]);
+      su[i / 64][i % 64] = to_f32(kBack ? dy[row * in.H * in.P + c] : in.x[row * in.xs + c]);
     }
     __syncthreads();
-    if constexpr (MODE == kAdjoint) {
+    if constexpr (kBack) {
       for (int t = n - 1; t >= 0; --t) {
-        if ((b0 + t) % kChunk == kChunk - 1 || b0 + t == len - 1) {
+        if (MODE == kAdjoint && ((b0 + t) % kChunk == kChunk - 1 || b0 + t == len - 1)) {
           float *d = dump + ((slot0 + (b0 + t) / kChunk) * in.H + h) * (long long)N * in.P + pt * 64 + p;
 #pragma unroll
           for (int i = 0; i < R; ++i) d[(long long)(q * R + i) * in.P] = st[i];
@@ -153,25 +221,45 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
       }
     }
   }
-  if (MODE != kStates) {
+  float *dst = nullptr;
+  if constexpr (kAdd) {
+    dst = ends.state + at_run;
+    if (tid < 32) {  // the lanes of the staged tokens
 #pragma unroll
-    for (int i = 0; i < R; ++i) out_state[at + (long long)(q * R + i) * in.P] = st[i];
+      for (int o = 16; o > 0; o >>= 1) decay += __shfl_xor_sync(0xffffffffu, decay, o);
+      if (tid == 0 && pt == 0) ends.decay[slot * in.H + h] = (float)exp(decay);
+    }
+  } else if (MODE != kStates && last_run) {
+    dst = out_state + at;
+  }
+  if (dst) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) dst[(long long)(q * R + i) * in.P] = st[i];
   }
 }
 
 template <typename T, int N>
 __global__ void __launch_bounds__(256)
-forward_kernel(const In<T> in, T *__restrict__ y, float *out_state, unsigned *err) {
-  sweep<T, N, kForward>(in, nullptr, nullptr, y, out_state, nullptr, err);
+forward_kernel(const In<T> in, int seg_chunks, Ends ends, T *__restrict__ y, float *out_state, unsigned *err) {
+  sweep<T, N, kForward>(in, nullptr, in.state_in, seg_chunks, ends, y, out_state, nullptr, err);
+}
+template <typename T, int N>
+__global__ void __launch_bounds__(256)
+adds_kernel(const In<T> in, const T *__restrict__ dy, int seg_chunks, Ends fwd, Ends rev, unsigned *err) {
+  if (blockIdx.y == 0) sweep<T, N, kAdds>(in, nullptr, nullptr, seg_chunks, fwd, nullptr, nullptr, nullptr, err);
+  else sweep<T, N, kAddsBack>(in, dy, nullptr, seg_chunks, rev, nullptr, nullptr, nullptr, err);
 }
 // The gradient's two sweeps, side by side: a sweep is a chain of tokens that
 // leaves most of an SM idle.
 template <typename T, int N>
 __global__ void __launch_bounds__(256)
 boundaries_kernel(const In<T> in, const T *__restrict__ dy, const float *__restrict__ dstate_out,
-                  float *__restrict__ states, float *__restrict__ adjoints, float *dstate_in, unsigned *err) {
-  if (blockIdx.y == 0) sweep<T, N, kStates>(in, nullptr, nullptr, nullptr, nullptr, states, err);
-  else sweep<T, N, kAdjoint>(in, dy, dstate_out, nullptr, dstate_in, adjoints, err);
+                  int seg_chunks, Ends fwd, Ends rev, float *__restrict__ states,
+                  float *__restrict__ adjoints, float *dstate_in, unsigned *err) {
+  if (blockIdx.y == 0)
+    sweep<T, N, kStates>(in, nullptr, in.state_in, seg_chunks, fwd, nullptr, nullptr, states, err);
+  else
+    sweep<T, N, kAdjoint>(in, dy, dstate_out, seg_chunks, rev, nullptr, dstate_in, adjoints, err);
 }
 
 // One decode token of one (sequence, head, 64-column tile).  Bound by the

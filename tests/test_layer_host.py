@@ -176,9 +176,9 @@ def test_scan_workspaces(lib):
     size = lib.lib.gdn_scan_prefill_workspace_bytes
     assert size(2, 70, 4, 64, 1, 128, BF16, 0) == 0            # two chunks a sequence
     assert size(256, 8192, 32, 64, 1, 128, BF16, 0) == 0       # units enough for every SM
-    assert size(1, 8192, 1, 64, 1, 128, F32, 0) == 0           # CUDA cores: no runs
     # 128 chunks in 32 runs of four: a state and a decay a run (16-byte steps)
-    assert size(1, 8192, 1, 64, 1, 128, BF16, 0) == 32 * 128 * 64 * 4 + 32 * 4
+    for dtype in (BF16, F32):
+        assert size(1, 8192, 1, 64, 1, 128, dtype, 0) == 32 * 128 * 64 * 4 + 32 * 4
     assert size(1, 8192, 1, 96, 1, 128, BF16, 0) == 0
     back = lib.lib.gdn_scan_backward_workspace_bytes
     # fp32: states and adjoints of 2 x 2 chunks, dB and dC of every head, parts
