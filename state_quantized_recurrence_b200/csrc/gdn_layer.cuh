@@ -39,15 +39,6 @@ __device__ __forceinline__ uint32_t bf2_set(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&p);
 }
 template <>
-struct Vec<__nv_bfloat16, 2> {
-  uint32_t raw;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { raw = *reinterpret_cast<const uint32_t *>(p); }
-  __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint32_t *>(p) = raw; }
-  __device__ __forceinline__ void zero() { raw = 0; }
-  __device__ __forceinline__ void get(float (&f)[2]) const { bf2_get(raw, f[0], f[1]); }
-  __device__ __forceinline__ void set(const float (&f)[2]) { raw = bf2_set(f[0], f[1]); }
-};
-template <>
 struct Vec<__nv_bfloat16, 4> {
   uint2 raw;
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) { raw = *reinterpret_cast<const uint2 *>(p); }

@@ -160,3 +160,42 @@ def test_empty_and_repeats_and_graph(cuda_lib):
     torch.cuda.synchronize()
     for a, b, c in zip(want, again, out):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("d", [20000, 32768])
+def test_longest_rows(cuda_lib, d):
+    x, w, res, z, dy, dr = make(7, (3, d), BF16, True, True)
+    y, s = cuda_lib.gdn_norm(x, w, residual=res, gate=z)
+    want, _ = ref.norm(x, w, res, z, dtype=BF16)
+    ref.within(y, want, want.abs(), d // 8 + 74, "y")
+    q, _ = cuda_lib.gdn_norm(x, w, residual=res, gate=z, qdq="fp8_row")
+    step = torch.maximum(want.abs() * 2.0 ** -4, q.scales.double().cpu()[:, None] * 2.0 ** -10)
+    assert ((q.dequantize().double().cpu() - want).abs() <= step * (1 + 1e-3)).all()
+    dx, dw, dz = cuda_lib.gdn_norm_backward(s, w, dy, gate=z, dresidual=dr)
+    g, m = ref.norm_grad(s, w, dy, z, dr), ref.norm_grad(s, w, dy, z, dr, mag=True)
+    ref.within(dx, g[0], m[0], 3 * (d // 8 + 74), "dx")
+    ref.within(dw, g[1], m[1], d // 8 + 74 + 3, "dweight")
+    ref.within(dz, g[2], m[2] + (dy.double().cpu() * ref.norm(s, w)[0]).abs() * 1.1, d // 8 + 74,
+               "dgate")
+    with pytest.raises(cuda_lib.GdnError):
+        cuda_lib.gdn_norm(torch.zeros(1, 32776, dtype=BF16, device="cuda"),
+                          torch.ones(32776, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_weights_off_the_vector_grid(cuda_lib, dtype):
+    """A weight that starts 4 bytes past a 16-byte boundary gives the bits of
+    an aligned copy; so does a convolution's."""
+    x, w, _, _, dy, _ = make(8, (5, 256), dtype, False, False)
+    off = torch.cat([w[:1], w])[1:]
+    assert off.data_ptr() % 16 == 4 and off.is_contiguous()
+    assert torch.equal(cuda_lib.gdn_norm(x, w)[0], cuda_lib.gdn_norm(x, off)[0])
+    for a, b in zip(cuda_lib.gdn_norm_backward(x, w, dy)[:2],
+                    cuda_lib.gdn_norm_backward(x, off, dy)[:2]):
+        assert torch.equal(a, b)
+    taps = torch.randn(256, 4, device="cuda")
+    far = torch.cat([taps.flatten()[:1], taps.flatten()])[1:].view(256, 4)
+    assert far.data_ptr() % 16 == 4
+    for a, b in zip(cuda_lib.gdn_conv_prefill(x[None], taps),
+                    cuda_lib.gdn_conv_prefill(x[None], far)):
+        assert torch.equal(a, b)

@@ -91,8 +91,9 @@ def test_long_sequences_of_few_heads(cuda_lib, T, n, N, dtype):
     check(cuda_lib, T, n, 2, 64, 1, N, dtype, state=True)
 
 
-def test_state_in_place_over_runs(cuda_lib):
-    (x, raw, A, B, C), D, bias, st, _, _ = make(12, (2, 900), 2, 128, 1, 64, BF16, 2, True)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_state_in_place_over_runs(cuda_lib, dtype):
+    (x, raw, A, B, C), D, bias, st, _, _ = make(12, (2, 900), 2, 128, 1, 64, dtype, 2, True)
     y0, s0 = cuda_lib.gdn_scan_prefill(x, raw, A, B, C, D=D, dt_bias=bias, state_in=st)
     for _ in range(20):
         s, y = st.clone(), torch.empty_like(y0)
