@@ -217,7 +217,9 @@ constexpr int kSweepThreads = 256;
 // Two barriers a chunk: the tiles of B and x are double, C's is filled again
 // as soon as M and C S_0 have been formed.  With four warps that hold all of
 // N (168 registers, three CTAs an SM) packed batches ran the same (0.75 ms),
-// one long sequence slower (0.11 ms against 0.08).
+// one long sequence slower (0.11 ms against 0.08).  With sixteen that hold a
+// quarter each, a CTA alone on its SM ran no faster either (4 x 4096 tokens x
+// 16 heads of 128: 289 us against 279).
 //
 // REV: the adjoint G backwards over the chunks, G_0 = e^{c_n} G_n + sum_i
 // e^{c_i} C_i dy_i^T, with C in B's place, dy in x's and e^{c_i} in w's.
