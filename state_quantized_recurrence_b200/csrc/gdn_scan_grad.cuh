@@ -1,16 +1,20 @@
 // Gradient of the scan's chunks for bf16 inputs on the tensor cores: the
-// algebra of chunk_grad_kernel with mma.sync products of bf16 pieces.  What is
-// rounded to bf16 in the end (dx, dB, dC, the step's gradient) takes pairs
-// (2^-17 relative) for M and W; what dA and ddt_bias add up over all tokens is
-// kept to fp32's own rounding: Z stays fp32, x_t . du_t is taken from Z's
+// algebra of chunk_grad_kernel with mma.sync products of bf16 pieces.  dx takes
+// a pair (2^-17 relative) for M.  dB and dC, which add up a group's heads, take
+// three pieces of W, and a head's products are formed by themselves and added
+// in fp32: with pairs, and the tensor pipe's truncating sums running on over
+// 16 heads, the two differed from the rounded 64-bit gradient by 1.0e-4 to
+// 1.4e-4 (2-norm) where a 32-bit form differs by 2.5e-5; now by 2.5e-5 to
+// 4.6e-5, in the same time (388 us the call).  A third piece of M would take dx
+// from 7.7e-5 to 3.9e-5 for 10 us.  What dA and ddt_bias add up over all tokens
+// is kept to fp32's own rounding: Z stays fp32, x_t . du_t is taken from Z's
 // columns instead of du, and the states and adjoints come in three pieces
 // (with two, dA was up to 8e-6 off; the third costs 45 us of the 232 below).
 //
 // A CTA of sixteen warps takes one chunk and a range of one group's heads.
-// S = C B^T is formed once; dB and dC are summed over the heads in the
-// accumulators, so that neither leaves the SM before it is whole (with the
-// heads split over several CTAs, their fp32 parts are added afterwards in
-// order).
+// S = C B^T is formed once; dB and dC are summed over the heads in registers,
+// so that neither leaves the SM before it is whole (with the heads split over
+// several CTAs, their fp32 parts are added afterwards in order).
 //
 // 2 x 4096 tokens x 16 heads, N = 128, P = 64: 232 us, 27 thousand cycles a
 // head and chunk for 6.5 of tensor pipe and about 12 of shared-memory pipe
@@ -32,13 +36,13 @@ struct GradSmem {
   static constexpr uint32_t H = Y + P / 64 * kTileBytes<64>;  // hi, lo: [64 p][N]
   static constexpr uint32_t G = H + 2 * kTileBytes<N>;
   static constexpr uint32_t M = G + 2 * kTileBytes<N>;     // hi, lo
-  static constexpr uint32_t W = M + 2 * kTileBytes<64>;
-  static constexpr uint32_t Z = W + 2 * kTileBytes<64>;    // fp32 [64][65]
+  static constexpr uint32_t W = M + 2 * kTileBytes<64>;    // hi, mid, lo
+  static constexpr uint32_t Z = W + 3 * kTileBytes<64>;    // fp32 [64][65]
   static constexpr uint32_t kZ = 64 * 65 * 4 > kTileBytes<N> ? 64 * 65 * 4 : kTileBytes<N>;
   static constexpr uint32_t V = (Z + kZ + 15) / 16 * 16;
   // the third pieces of H and G take the places of W and Z once those are read
   static constexpr uint32_t H3 = W, G3 = Z;
-  static_assert(kTileBytes<N> <= 2 * kTileBytes<64>, "H's third piece fits into W");
+  static_assert(kTileBytes<N> <= 3 * kTileBytes<64>, "H's third piece fits into W");
   // row sums by warp column: r, q (4 each), Z block sums [4][64], Z's part of
   // l, l, gh and dD by warp
   struct Rows {
@@ -46,6 +50,7 @@ struct GradSmem {
   };
   static constexpr uint32_t D = V + (sizeof(Rows) + 15) / 16 * 16;
   static constexpr uint32_t bytes = D + 2 * sizeof(Decays);
+  static_assert(bytes <= 227 * 1024, "a CTA's shared memory");
 };
 
 __device__ __forceinline__ float quad_sum(float v) {
@@ -185,14 +190,15 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
             wv[u] = k * d * m.dt[c + u];
             sZ[r * 65 + c + u] = mv[u] * k;
           }
-          uint32_t hi, lo;
+          uint32_t hi, mid, lo;
           const uint32_t at = tile_at<64>(0, r, c / 8) + q * 4;
           split2(mv[0], mv[1], hi, lo);
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(sM + at), "r"(hi) : "memory");
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(sM + kTileBytes<64> + at), "r"(lo) : "memory");
-          split2(wv[0], wv[1], hi, lo);
+          split3(wv[0], wv[1], hi, mid, lo);
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + at), "r"(hi) : "memory");
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + kTileBytes<64> + at), "r"(lo) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + kTileBytes<64> + at), "r"(mid) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sW + 2 * kTileBytes<64> + at), "r"(lo) : "memory");
         }
       }
     } else {  // above the diagonal: Z alone is read there
@@ -214,45 +220,38 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       }
       rs.zb[b][c] = s;
     }
-    // what needs no state: dC += W B, dB += W^T C
+    // what needs no state: dC += W B (side 0), dB += W^T C (side 1)
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint32_t b[kJ][4];
-      const bool need_c = kk <= gr / 16, need_b = kk >= gr / 16;
-      if (need_c) {
+    for (int side = 0; side < 2; ++side) {
+      float T[2 * kJ][4];
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) ldsm4t(block_rows<N>(sB, 16 * kk, gc / 8 + 2 * j, lane), b[j]);
+      for (int j = 0; j < 2 * kJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 1; ++i) {
+        for (int e = 0; e < 4; ++e) T[j][e] = 0.0f;
 #pragma unroll
-          for (int piece = 0; piece < 2; ++piece) {
-            uint32_t a[4];
-            ldsm4(block_rows<64>(sW + piece * kTileBytes<64>, gr + 16 * i, 2 * kk, lane), a);
+      for (int kk = 0; kk < 4; ++kk) {
+        if (side ? kk < gr / 16 : kk > gr / 16) continue;  // above the diagonal
+        uint32_t b[kJ][4];
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-              mma16816(aC[i][2 * j], a, b[j][0], b[j][1]);
-              mma16816(aC[i][2 * j + 1], a, b[j][2], b[j][3]);
-            }
+        for (int j = 0; j < kJ; ++j) ldsm4t(block_rows<N>(side ? sC : sB, 16 * kk, gc / 8 + 2 * j, lane), b[j]);
+#pragma unroll
+        for (int piece = 0; piece < 3; ++piece) {
+          const uint32_t tW = sW + piece * kTileBytes<64>;
+          uint32_t a[4];
+          if (side) ldsm4t(block_cols<64>(tW, 16 * kk, gr / 8, lane), a);
+          else ldsm4(block_rows<64>(tW, gr, 2 * kk, lane), a);
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            mma16816(T[2 * j], a, b[j][0], b[j][1]);
+            mma16816(T[2 * j + 1], a, b[j][2], b[j][3]);
           }
         }
       }
-      if (need_b) {
+      float(&acc)[2 * kJ][4] = side ? aB[0] : aC[0];
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) ldsm4t(block_rows<N>(sC, 16 * kk, gc / 8 + 2 * j, lane), b[j]);
+      for (int j = 0; j < 2 * kJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 1; ++i) {
-#pragma unroll
-          for (int piece = 0; piece < 2; ++piece) {
-            uint32_t a[4];
-            ldsm4t(block_cols<64>(sW + piece * kTileBytes<64>, 16 * kk, (gr + 16 * i) / 8, lane), a);
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-              mma16816(aB[i][2 * j], a, b[j][0], b[j][1]);
-              mma16816(aB[i][2 * j + 1], a, b[j][2], b[j][3]);
-            }
-          }
-        }
-      }
+        for (int e = 0; e < 4; ++e) acc[j][e] += T[j][e];
     }
     __syncthreads();  // Z's sums are there, W has been read
     fetch_third(states, base + L::H3, h, 0);

@@ -1,0 +1,64 @@
+"""The selective scan over thousands of tokens and many heads, norm-wise
+against the chunked 64-bit form: what element-wise bounds that count every
+token's roundings cannot see.
+
+A bf16 output that is the rounding of a value within a relative eps (2-norm)
+of the exact one differs from the exact one's rounding only where the two
+straddle a boundary, with probability |d| / step each; a step is 2^-7 of the
+value at most, so the squared 2-norm of what differs is at most sum |d| step <=
+2^-7 eps of the output's.  fp32 outputs are compared directly."""
+
+import math
+
+import pytest
+import torch
+
+import layer_long as long
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def make(seed, lead, n, H, P, G, N, dtype, step, decay, spread=1.0):
+    """Inputs as a projection gives them, the steps around `step` (their
+    logarithm spread by `spread`), A between `decay`'s two values."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, B, C = r(*lead, H, P).to(dtype), r(*lead, G, N).to(dtype), r(*lead, G, N).to(dtype)
+    raw = (r(*lead, H) * spread).to(dtype)
+    A = -(torch.rand(H, generator=g, device="cuda") * (decay[1] - decay[0]) + decay[0])
+    bias = torch.full((H,), math.log(math.expm1(step)), device="cuda")
+    return dict(x=x, raw=raw, A=A, B=B, C=C, D=r(H), bias=bias, state=r(n, H, N, P),
+                dy=r(*lead, H, P).to(dtype), dlast=r(n, H, N, P))
+
+
+def prefill(lib, t, cu=None):
+    return lib.gdn_scan_prefill(t["x"], t["raw"], t["A"], t["B"], t["C"], D=t["D"],
+                                dt_bias=t["bias"], state_in=t["state"], cu_seqlens=cu)
+
+
+def backward(lib, t, cu=None):
+    return lib.gdn_scan_backward(t["x"], t["raw"], t["A"], t["B"], t["C"], t["dy"], D=t["D"],
+                                 dt_bias=t["bias"], state_in=t["state"], cu_seqlens=cu,
+                                 dstate_out=t["dlast"])
+
+
+def args(t, cu=None):
+    return tuple(t[k] for k in ("x", "raw", "A", "B", "C", "D", "bias", "state")) + (cu,)
+
+
+def rounding(eps):
+    return math.sqrt(eps * 2.0 ** -7)
+
+
+def test_gradients_summed_over_many_heads(cuda_lib):
+    """One CTA takes a chunk's sixteen heads.  dB and dC are fp32 sums of
+    products whose operands carry 2^-25; a head's products are twelve sums in
+    the tensor pipe, which truncates (2^-24 each on average), and four more
+    stand for the decays: eps = 2^-20.  dx has M in bf16 pairs, 2^-18."""
+    t = make(1, (2, 4096), 2, 16, 64, 1, 128, BF16, 0.01, (1.0, 16.0))
+    got = backward(cuda_lib, t)
+    want = long.scan_grad(*args(t), t["dy"], t["dlast"])[2:]
+    for i, name, eps in ((3, "dB", 2.0 ** -20), (4, "dC", 2.0 ** -20), (0, "dx", 2.0 ** -18),
+                         (1, "ddt", 2.0 ** -18)):
+        assert long.off(got[i], want[i].to(BF16)) <= rounding(eps), name
