@@ -440,35 +440,11 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
       }
     }
 
-    // Both products that read x.  The sweeps of the gradient sum what the
-    // chunk adds to the state by itself: the tensor pipe truncates a sum at its
-    // own magnitude, and twelve of those a chunk at the state's cost a slowly
-    // forgetting one 1.5e-6 of its adjoint.  The forward sweep, whose states
-    // stay within 4e-7, has no registers for it (spills: 281 -> 349 us on 4 x
-    // 4096 tokens x 16 heads) and adds to the decayed state itself.
-    constexpr bool kApart = LEAVE != kY;
-    const float all = m.all;
-    const uint64_t all2 = f2_pack(all, all);
-    float add[kApart ? kT : 1][4];
-    auto sum = [&](int i) -> float(&)[4] {
-      if constexpr (kApart) return add[i];
-      else return st[i];
-    };
+    if constexpr (LEAVE == kY) {  // y += M x, and its rows leave
 #pragma unroll
-    for (int i = 0; i < kT; ++i) {
-      if constexpr (kApart) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) add[i][e] = 0.0f;
-      } else {
-        f2_unpack(f2_mul(f2_pack(st[i][0], st[i][1]), all2), st[i][0], st[i][1]);
-        f2_unpack(f2_mul(f2_pack(st[i][2], st[i][3]), all2), st[i][2], st[i][3]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t x[4];  // (p, p + 8) x (j, j + 8) of x^T
-      ldsm4t(block_cols<64>(sX, 16 * j, 2 * pw, lane), x);
-      if constexpr (LEAVE == kY) {
+      for (int j = 0; j < 4; ++j) {
+        uint32_t x[4];  // (p, p + 8) x (j, j + 8) of x^T
+        ldsm4t(block_cols<64>(sX, 16 * j, 2 * pw, lane), x);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (j > i + 2 * nh) continue;  // above the diagonal
@@ -481,48 +457,6 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
           }
         }
       }
-      const float *wv = REV ? m.gam : m.w;
-      const float2 wa = *reinterpret_cast<const float2 *>(wv + 16 * j + 2 * q);
-      const float2 wb = *reinterpret_cast<const float2 *>(wv + 16 * j + 8 + 2 * q);
-      uint32_t u0[4], u1[4], u2[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float lo, hi;
-        bf2_get(x[e], lo, hi);
-        const float2 w = e < 2 ? wa : wb;
-        split3(lo * w.x, hi * w.y, u0[e], u1[e], u2[e]);
-      }
-#pragma unroll
-      for (int i = 0; i < kT / 2; i += 2) {
-        uint32_t b[2][4];  // (j, j + 8) x (n, n + 8)
-        ldsm4t(block_rows<N>(sB, 16 * j, nh * (N / 16) + 2 * i, lane), b[0]);
-        ldsm4t(block_rows<N>(sB, 16 * j, nh * (N / 16) + 2 * i + 2, lane), b[1]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mma16816(sum(2 * (i + e)), u0, b[e][0], b[e][1]);
-          mma16816(sum(2 * (i + e) + 1), u0, b[e][2], b[e][3]);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mma16816(sum(2 * (i + e)), u1, b[e][0], b[e][1]);
-          mma16816(sum(2 * (i + e) + 1), u1, b[e][2], b[e][3]);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mma16816(sum(2 * (i + e)), u2, b[e][0], b[e][1]);
-          mma16816(sum(2 * (i + e) + 1), u2, b[e][2], b[e][3]);
-        }
-      }
-    }
-    if constexpr (kApart) {
-#pragma unroll
-      for (int i = 0; i < kT; ++i) {
-        f2_unpack(f2_fma(f2_pack(st[i][0], st[i][1]), all2, f2_pack(add[i][0], add[i][1])), st[i][0], st[i][1]);
-        f2_unpack(f2_fma(f2_pack(st[i][2], st[i][3]), all2, f2_pack(add[i][2], add[i][3])), st[i][2], st[i][3]);
-      }
-    }
-    if (LEAVE == kEnds) run_decay *= all;
-    if constexpr (LEAVE == kY) {
       const int n = rows_in(c);
       __nv_bfloat16 *yo = y + (row_of(c) * in.H + h) * in.P + pt * 64 + pw * 16 + 2 * q;
 #pragma unroll
@@ -542,6 +476,65 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
           }
         }
     }
+
+    // What the chunk adds to the state is summed by itself: the tensor pipe
+    // truncates a sum at its own magnitude, and twelve of those a chunk at the
+    // state's took 3.4e-5 from states that remember most of 8192 tokens (now
+    // 3e-7).  Behind y's stores, whose registers it takes; the barrier of the
+    // warp keeps the compiler from drawing its loads up in front of them, which
+    // spills (64 packed sequences, 125 thousand tokens, 16 heads of 64: 783 us
+    // with it, 825 without, 778 with the sums on top of the state).
+    __syncwarp();
+    const float all = m.all;
+    const uint64_t all2 = f2_pack(all, all);
+    float add[kT][4];
+#pragma unroll
+    for (int i = 0; i < kT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) add[i][e] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t x[4];
+      ldsm4t(block_cols<64>(sX, 16 * j, 2 * pw, lane), x);
+      const float *wv = REV ? m.gam : m.w;
+      const float2 wa = *reinterpret_cast<const float2 *>(wv + 16 * j + 2 * q);
+      const float2 wb = *reinterpret_cast<const float2 *>(wv + 16 * j + 8 + 2 * q);
+      uint32_t u0[4], u1[4], u2[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        bf2_get(x[e], lo, hi);
+        const float2 w = e < 2 ? wa : wb;
+        split3(lo * w.x, hi * w.y, u0[e], u1[e], u2[e]);
+      }
+#pragma unroll
+      for (int i = 0; i < kT / 2; i += 2) {
+        uint32_t b[2][4];  // (j, j + 8) x (n, n + 8)
+        ldsm4t(block_rows<N>(sB, 16 * j, nh * (N / 16) + 2 * i, lane), b[0]);
+        ldsm4t(block_rows<N>(sB, 16 * j, nh * (N / 16) + 2 * i + 2, lane), b[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mma16816(add[2 * (i + e)], u0, b[e][0], b[e][1]);
+          mma16816(add[2 * (i + e) + 1], u0, b[e][2], b[e][3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mma16816(add[2 * (i + e)], u1, b[e][0], b[e][1]);
+          mma16816(add[2 * (i + e) + 1], u1, b[e][2], b[e][3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mma16816(add[2 * (i + e)], u2, b[e][0], b[e][1]);
+          mma16816(add[2 * (i + e) + 1], u2, b[e][2], b[e][3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kT; ++i) {
+      f2_unpack(f2_fma(f2_pack(st[i][0], st[i][1]), all2, f2_pack(add[i][0], add[i][1])), st[i][0], st[i][1]);
+      f2_unpack(f2_fma(f2_pack(st[i][2], st[i][3]), all2, f2_pack(add[i][2], add[i][3])), st[i][2], st[i][3]);
+    }
+    if (LEAVE == kEnds) run_decay *= all;
     if (more && LEAVE != kY && warp == 7) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
   }
 

@@ -62,3 +62,21 @@ def test_gradients_summed_over_many_heads(cuda_lib):
     for i, name, eps in ((3, "dB", 2.0 ** -20), (4, "dC", 2.0 ** -20), (0, "dx", 2.0 ** -18),
                          (1, "ddt", 2.0 ** -18)):
         assert long.off(got[i], want[i].to(BF16)) <= rounding(eps), name
+
+
+@pytest.mark.parametrize("n,T,H,step,decay,spread", [
+    (4, 4096, 32, 1e-3, (1.0, 1.0), 1.0), (4, 8192, 32, 1e-4, (0.1, 0.1), 0.0),
+    (2, 4096, 64, 1e-2, (1.0, 16.0), 1.0)])
+def test_states_of_long_prompts(cuda_lib, n, T, H, step, decay, spread):
+    """The state that a prompt leaves, in 32 bits, from quick forgetting to
+    none: a chunk adds twelve sums in the tensor pipe (2^-23 at most each) and
+    one rounding of the state; the decays of the chunks are products of
+    T / 64 of them, whose roundings (2^-24) add up like their root; the step
+    and its logarithm's bias are off by 2^-21 at most."""
+    t = make(3, (n, T), n, H, 64, 1, 64, BF16, step, decay, spread)
+    y, last = prefill(cuda_lib, t)
+    want = long.scan(*(v if v is None else v.double() for v in args(t)))
+    eps = (12 * 2.0 + 1) * 2.0 ** -24 + math.sqrt(T / 64) * 2.0 ** -24 + 2.0 ** -21
+    assert long.off(last, want[1]) <= eps
+    # y: M and the state in bf16 pairs, 2^-18
+    assert long.off(y, want[0].to(BF16)) <= rounding(2.0 ** -18)
