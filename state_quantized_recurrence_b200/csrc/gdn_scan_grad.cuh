@@ -98,6 +98,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
   }
   const long long row0 = t.start + (long long)t.tile * 64;
   const long long np = (long long)N * in.P;
+  float none = 0.0f;
 
   auto fetch_states = [&](int h, int pt) {
     const __nv_bfloat16 *s = states + (slot * in.H + h) * kPieces * np + (long long)pt * 64 * N;
@@ -122,7 +123,8 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
   fetch_tile<N, kGradThreads>(sC, in.C + row0 * in.cs + grp * N, in.cs, n, tid);
   if (h0 < h1) {
     fetch_head(h0);
-    if (warp == 0) decays_of(raw_steps(in, row0, n, h0), n, in.A[h0], in.bias ? in.bias[h0] : 0.0f, dec[0]);
+    if (warp == 0)
+      decays_of<false>(raw_steps(in, row0, n, h0), n, in.A[h0], in.bias ? in.bias[h0] : 0.0f, dec[0], none);
   }
   copy_commit();
 
@@ -436,8 +438,8 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       fetch_head(h + 1);
       copy_commit();
       if (warp == 15)
-        decays_of(raw_steps(in, row0, n, h + 1), n, in.A[h + 1], in.bias ? in.bias[h + 1] : 0.0f,
-                  dec[(h + 1 - h0) & 1]);
+        decays_of<false>(raw_steps(in, row0, n, h + 1), n, in.A[h + 1], in.bias ? in.bias[h + 1] : 0.0f,
+                         dec[(h + 1 - h0) & 1], none);
     }
     // l_t, four threads a token
     if (tid < 256) {

@@ -129,6 +129,7 @@ struct alignas(16) Decays {  // two of them lie side by side and are read in pai
   float del[64];          // e^{c_n - c_t}
   float w[64];            // del * dt
   float all;              // e^{c_n}: the decay of the state over the chunk
+  float log;              // c_n
 };
 // 2^v with its subnormals (the decays of whole chunks reach them).
 __device__ __forceinline__ float exp2_of(double v) {
@@ -150,8 +151,11 @@ __device__ __forceinline__ RawSteps raw_steps(const In<__nv_bfloat16> &in, long 
     r.v[k] = t + k < n ? in.raw[(row0 + t + k) * in.rs + h] : __nv_bfloat16(0.0f);
   return r;
 }
-// By one warp; tokens past n have step 0 and decay 1.
-__device__ __forceinline__ void decays_of(const RawSteps &raw, int n, float A, float bias, Decays &m) {
+// By one warp; tokens past n have step 0 and decay 1.  CHAIN: `all` is a step
+// of a chain of chunks, whose roundings `carry` takes along.
+template <bool CHAIN>
+__device__ __forceinline__ void decays_of(const RawSteps &raw, int n, float A, float bias, Decays &m,
+                                          float &carry) {
   const int lane = threadIdx.x & 31;
   double a[2];
   float dt[2];
@@ -191,7 +195,14 @@ __device__ __forceinline__ void decays_of(const RawSteps &raw, int n, float A, f
     m.del[t] = d;
     m.w[t] = d * dt[k];
   }
-  if (lane == 0) m.all = exp2_of(total);
+  if (lane == 0) {
+    if constexpr (CHAIN) {
+      m.log = (float)(total * 0.6931471805599453);
+      m.all = exp_step(m.log, carry);
+    } else {
+      m.all = exp2_of(total);
+    }
+  }
 }
 
 // What a sweep leaves behind.
@@ -282,7 +293,7 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
   auto row_of = [&](int c) { return t.start + (long long)c * 64; };
   auto rows_in = [&](int c) { return (int)min(64LL, row_end - row_of(c)); };
   const int total = c1 - c0;
-  float run_decay = 1.0f;
+  float run_log = 0.0f, carry = 0.0f;
 
   if (total > 0) {
     const int c = chunk_at(0);
@@ -291,7 +302,8 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
     fetch_tile<N, kSweepThreads>(sB0, Bp + row_of(c) * Bs, Bs, rows_in(c), tid);
     fetch_tile<64, kSweepThreads>(sX0, Xp + row_of(c) * Xs, Xs, rows_in(c), tid);
     copy_commit();
-    if (warp == 7) decays_of(raw_steps(in, row_of(c), rows_in(c), h), rows_in(c), A, bias, dec[0]);
+    if (warp == 7)
+      decays_of<true>(raw_steps(in, row_of(c), rows_in(c), h), rows_in(c), A, bias, dec[0], carry);
   }
   const float Dh = LEAVE == kY && in.D ? in.D[h] : 0.0f;
 
@@ -389,7 +401,7 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(at0 + 8 * kRowBytes<64> + kTileBytes<64>), "r"(lo) : "memory");
         }
       }
-      if (warp == 7 && more) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
+      if (warp == 7 && more) decays_of<true>(raw, rows_in(cn), A, bias, dec[(k + 1) & 1], carry);
       // C S_0 over this warp's half of N, the state's pieces straight from
       // the accumulators
 #pragma unroll
@@ -534,15 +546,15 @@ __device__ __forceinline__ void sweep_run(const In<__nv_bfloat16> &in, const __n
       f2_unpack(f2_fma(f2_pack(st[i][0], st[i][1]), all2, f2_pack(add[i][0], add[i][1])), st[i][0], st[i][1]);
       f2_unpack(f2_fma(f2_pack(st[i][2], st[i][3]), all2, f2_pack(add[i][2], add[i][3])), st[i][2], st[i][3]);
     }
-    if (LEAVE == kEnds) run_decay *= all;
-    if (more && LEAVE != kY && warp == 7) decays_of(raw, rows_in(cn), A, bias, dec[(k + 1) & 1]);
+    if (LEAVE == kEnds) run_log += m.log;
+    if (more && LEAVE != kY && warp == 7) decays_of<true>(raw, rows_in(cn), A, bias, dec[(k + 1) & 1], carry);
   }
 
   if (LEAVE == kChunks && tid < 64 * kPieces) sm100::bulk_wait_all();
   float *dst = nullptr;
   if (LEAVE == kEnds) {
     dst = ends.state + (slot * in.H + h) * np + p0;
-    if (tid == 0 && pt == 0) ends.decay[slot * in.H + h] = run_decay;
+    if (tid == 0 && pt == 0) ends.log_decay[slot * in.H + h] = run_log;
   } else if (last_seg && out_state) {
     dst = out_state + ((long long)t.seq * in.H + h) * np + p0;
   }

@@ -30,13 +30,43 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
+// e^x, x <= 0, as two floats.  Where more than 0.7 is kept, e^x - 1 is its
+// series (the first term left out is 2^-26 of it), and 1 + em and what that
+// drops are exact; a state that keeps less forgets the rounding with it.
+__device__ __forceinline__ void exp_pair(float x, float &hi, float &lo) {
+  float p = fmaf(x, 1.0f / 5040, 1.0f / 720);
+  p = fmaf(x, p, 1.0f / 120);
+  p = fmaf(x, p, 1.0f / 24);
+  p = fmaf(x, p, 1.0f / 6);
+  p = fmaf(x, p, 0.5f);
+  const float em = fmaf(x * x, p, x), one = 1.0f + em;
+  const bool near = x > -0.35f;
+  hi = near ? one : expf(x);
+  lo = near ? em - (one - 1.0f) : 0.0f;
+}
+// The decays of a chain of steps, one float each.  Rounded by itself (2^-24
+// relative), the same decay step after step takes a state that forgets little
+// as far off as the sum of those roundings, 6e-6 in 16384 tokens; here what a
+// step's rounding drops, relative to it, is carried into the next one, so
+// that the product of any number of them is within one rounding of the exact.
+__device__ __forceinline__ float exp_step(float x, float &carry) {
+  float one, lo;
+  exp_pair(x, one, lo);
+  const bool near = x > -0.35f;
+  lo = near ? fmaf(one, carry, lo) : 0.0f;
+  const float hi = one + lo;
+  carry = near ? __fdividef(lo - (hi - one), hi) : 0.0f;
+  return hi;
+}
+
 struct Ends {           // of the runs, where sequences are cut into several
   float *state;         // [run slot][H][N][P]; NULL: one run a sequence
-  float *decay;         // [run slot][H]
+  float *log_decay;     // [run slot][H]
 };
 
 // From what each run adds to zero (kEnds) to the state that each run starts
-// from, in place: run k starts from decay_{k-1} start_{k-1} + added_{k-1}.
+// from, in place: run k starts from e^{log_decay_{k-1}} start_{k-1} +
+// added_{k-1}.
 // A thread follows four state elements through the runs of a sequence.
 // Bound by latency; it keeps every run from adding up all that went before
 // it.
@@ -59,17 +89,18 @@ __device__ __forceinline__ void start_states(const int *__restrict__ cu, int n_s
   const long long at = part * 1024 + threadIdx.x * 4;
   float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
   if (first) run = *reinterpret_cast<const float4 *>(first + (s * H + h) * np + at);
+  float carry = 0.0f;
   constexpr int kAhead = 8;  // runs loaded before the first is needed
   for (int k0 = 0; k0 < segs; k0 += kAhead) {
     float4 add[kAhead];
-    float d[kAhead];
+    float log_d[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int k = k0 + u;
       if (k >= segs - 1) continue;  // the last run adds to nobody
       const long long w = slot + (REV ? segs - 1 - k : k);
       add[u] = *reinterpret_cast<const float4 *>(ends.state + (w * H + h) * np + at);
-      d[u] = ends.decay[w * H + h];
+      log_d[u] = ends.log_decay[w * H + h];
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -78,10 +109,11 @@ __device__ __forceinline__ void start_states(const int *__restrict__ cu, int n_s
       const long long w = slot + (REV ? segs - 1 - k : k);
       *reinterpret_cast<float4 *>(ends.state + (w * H + h) * np + at) = run;
       if (k == segs - 1) break;
-      run.x = fmaf(d[u], run.x, add[u].x);
-      run.y = fmaf(d[u], run.y, add[u].y);
-      run.z = fmaf(d[u], run.z, add[u].z);
-      run.w = fmaf(d[u], run.w, add[u].w);
+      const float d = exp_step(log_d[u], carry);
+      run.x = fmaf(d, run.x, add[u].x);
+      run.y = fmaf(d, run.y, add[u].y);
+      run.z = fmaf(d, run.z, add[u].z);
+      run.w = fmaf(d, run.w, add[u].w);
     }
   }
 }
@@ -227,7 +259,7 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
     if (tid < 32) {  // the lanes of the staged tokens
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) decay += __shfl_xor_sync(0xffffffffu, decay, o);
-      if (tid == 0 && pt == 0) ends.decay[slot * in.H + h] = (float)exp(decay);
+      if (tid == 0 && pt == 0) ends.log_decay[slot * in.H + h] = (float)decay;
     }
   } else if (MODE != kStates && last_run) {
     dst = out_state + at;

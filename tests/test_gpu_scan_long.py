@@ -80,3 +80,20 @@ def test_states_of_long_prompts(cuda_lib, n, T, H, step, decay, spread):
     assert long.off(last, want[1]) <= eps
     # y: M and the state in bf16 pairs, 2^-18
     assert long.off(y, want[0].to(BF16)) <= rounding(2.0 ** -18)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,step", [(16384, 1e-5), (8192, 1e-4)])
+def test_a_state_that_forgets_almost_nothing(cuda_lib, T, step, dtype):
+    """The same small step in every token, and few heads, so that the sequence
+    is cut into runs: neither the chunks' nor the runs' decays may drift.  The
+    bound of test_states_of_long_prompts for bf16; fp32 rounds the state once
+    a token, T roundings of 2^-25 on average that add up like their root."""
+    t = make(4, (1, T), 1, 2, 64, 1, 64, dtype, step, (0.1, 0.1), 0.0)
+    last = prefill(cuda_lib, t)[1]
+    want = long.scan(*(v if v is None else v.double() for v in args(t)))[1]
+    if dtype == BF16:
+        eps = (12 * 2.0 + 1) * 2.0 ** -24 + math.sqrt(T / 64) * 2.0 ** -24 + 2.0 ** -21
+    else:
+        eps = math.sqrt(T) * 2.0 ** -25 + 2.0 ** -21
+    assert long.off(last, want) <= eps
