@@ -30,19 +30,21 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
-// e^x, x <= 0, as two floats.  Where more than 0.7 is kept, e^x - 1 is its
-// series (the first term left out is 2^-26 of it), and 1 + em and what that
-// drops are exact; a state that keeps less forgets the rounding with it.
+// e^x as two floats, neither of them negative and the second not zero
+// (an infinity times both stays one).  Where 0.7 to 1.4 is kept, e^x - 1 is
+// its series (the first term left out is 2^-26 of it), and 1 + em, rounded
+// towards zero, and what that drops are exact; a state that keeps less forgets
+// the rounding with it.
 __device__ __forceinline__ void exp_pair(float x, float &hi, float &lo) {
   float p = fmaf(x, 1.0f / 5040, 1.0f / 720);
   p = fmaf(x, p, 1.0f / 120);
   p = fmaf(x, p, 1.0f / 24);
   p = fmaf(x, p, 1.0f / 6);
   p = fmaf(x, p, 0.5f);
-  const float em = fmaf(x * x, p, x), one = 1.0f + em;
-  const bool near = x > -0.35f;
+  const float em = fmaf(x * x, p, x), one = __fadd_rz(1.0f, em);
+  const bool near = fabsf(x) < 0.35f;
   hi = near ? one : expf(x);
-  lo = near ? em - (one - 1.0f) : 0.0f;
+  lo = fmaxf(near ? em - (one - 1.0f) : 0.0f, 0x1p-126f);
 }
 // The decays of a chain of steps, one float each.  Rounded by itself (2^-24
 // relative), the same decay step after step takes a state that forgets little
@@ -52,7 +54,7 @@ __device__ __forceinline__ void exp_pair(float x, float &hi, float &lo) {
 __device__ __forceinline__ float exp_step(float x, float &carry) {
   float one, lo;
   exp_pair(x, one, lo);
-  const bool near = x > -0.35f;
+  const bool near = fabsf(x) < 0.35f;
   lo = near ? fmaf(one, carry, lo) : 0.0f;
   const float hi = one + lo;
   carry = near ? __fdividef(lo - (hi - one), hi) : 0.0f;
@@ -296,7 +298,10 @@ boundaries_kernel(const In<T> in, const T *__restrict__ dy, const float *__restr
 
 // One decode token of one (sequence, head, 64-column tile).  Bound by the
 // state's HBM traffic, N x 64 fp32 read and written once; B and C are read
-// by every head of a group and stay in the caches.
+// by every head of a group and stay in the caches.  The decay is two floats:
+// nothing but the state goes from token to token, so that the rounding of one
+// float, token after token, would add up (8e-6 in 600 tokens of steps 1e-4 at
+// A = -0.1).
 template <typename T, int N>
 __global__ void __launch_bounds__(256)
 decode_kernel(const In<T> in, float *state, T *__restrict__ y) {
@@ -312,23 +317,28 @@ decode_kernel(const In<T> in, float *state, T *__restrict__ y) {
   for (int i = 0; i < N / 16; ++i)
     v[i] = *reinterpret_cast<const float4 *>(st + (long long)(r + 16 * i) * in.P);
   const float dt = softplus(to_f32(in.raw[s * in.rs + h]) + (in.bias ? in.bias[h] : 0.0f));
-  const float a = expf(dt * in.A[h]);
+  float a, al;
+  exp_pair(dt * in.A[h], a, al);
   const float4 x = load4(in.x + s * in.xs + (long long)h * in.P + pt * 64 + c4 * 4);
   const T *bp = in.B + s * in.bs + g * N, *cp = in.C + s * in.cs + g * N;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const uint64_t a2 = f2_pack(a, a), al2 = f2_pack(al, al), x01 = f2_pack(x.x, x.y), x23 = f2_pack(x.z, x.w);
+  uint64_t acc01 = 0, acc23 = 0;
 #pragma unroll
   for (int i = 0; i < N / 16; ++i) {
     const float b = dt * to_f32(bp[r + 16 * i]), c = to_f32(cp[r + 16 * i]);
-    v[i].x = fmaf(a, v[i].x, b * x.x);
-    v[i].y = fmaf(a, v[i].y, b * x.y);
-    v[i].z = fmaf(a, v[i].z, b * x.z);
-    v[i].w = fmaf(a, v[i].w, b * x.w);
-    acc.x = fmaf(c, v[i].x, acc.x);
-    acc.y = fmaf(c, v[i].y, acc.y);
-    acc.z = fmaf(c, v[i].z, acc.z);
-    acc.w = fmaf(c, v[i].w, acc.w);
+    const uint64_t b2 = f2_pack(b, b), c2 = f2_pack(c, c);
+    uint64_t v01 = f2_pack(v[i].x, v[i].y), v23 = f2_pack(v[i].z, v[i].w);
+    v01 = f2_fma(a2, v01, f2_fma(al2, v01, f2_mul(b2, x01)));
+    v23 = f2_fma(a2, v23, f2_fma(al2, v23, f2_mul(b2, x23)));
+    acc01 = f2_fma(c2, v01, acc01);
+    acc23 = f2_fma(c2, v23, acc23);
+    f2_unpack(v01, v[i].x, v[i].y);
+    f2_unpack(v23, v[i].z, v[i].w);
     *reinterpret_cast<float4 *>(st + (long long)(r + 16 * i) * in.P) = v[i];
   }
+  float4 acc;
+  f2_unpack(acc01, acc.x, acc.y);
+  f2_unpack(acc23, acc.z, acc.w);
   part[r][c4] = acc;
   __syncthreads();
   if (tid < 64) {

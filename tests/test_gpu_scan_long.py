@@ -97,3 +97,32 @@ def test_a_state_that_forgets_almost_nothing(cuda_lib, T, step, dtype):
     else:
         eps = math.sqrt(T) * 2.0 ** -25 + 2.0 ** -21
     assert long.off(last, want) <= eps
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_single_tokens(cuda_lib, dtype):
+    """600 single tokens of the same small step: every one rounds the state
+    once, 600 roundings of 2^-25 on average that add up like their root; the
+    step's logarithm is off by 2^-21 at most."""
+    T = 600
+    t = make(5, (2, T), 2, 2, 64, 1, 128, dtype, 1e-4, (0.1, 0.1), 0.0)
+    s = t["state"].clone()
+    for i in range(T):
+        y = cuda_lib.gdn_scan_decode(t["x"][:, i], t["raw"][:, i], t["A"], t["B"][:, i],
+                                     t["C"][:, i], s, D=t["D"], dt_bias=t["bias"])
+    want = long.scan(*(v if v is None else v.double() for v in args(t)))
+    assert long.off(s, want[1]) <= math.sqrt(T) * 2.0 ** -25 + 2.0 ** -21
+    half = torch.finfo(dtype).eps / 2
+    assert long.off(y, want[0][:, -1]) <= half + 2.0 ** -20
+
+
+def test_infinite_states_stay_infinite(cuda_lib):
+    """Whatever a decay's second float is, an infinity in a state is kept."""
+    t = make(6, (1, 8), 1, 2, 64, 1, 64, BF16, 1e-3, (0.5, 4.0))
+    s = t["state"].clone()
+    s[0, 0, 3, 5], s[0, 1, 7, 9] = math.inf, -math.inf
+    for i in range(8):
+        cuda_lib.gdn_scan_decode(t["x"][:, i], t["raw"][:, i], t["A"], t["B"][:, i], t["C"][:, i],
+                                 s, D=t["D"], dt_bias=t["bias"])
+    assert s[0, 0, 3, 5] == math.inf and s[0, 1, 7, 9] == -math.inf
+    assert int((~s.isfinite()).sum()) == 2
