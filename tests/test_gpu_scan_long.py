@@ -126,3 +126,20 @@ def test_infinite_states_stay_infinite(cuda_lib):
                                  s, D=t["D"], dt_bias=t["bias"])
     assert s[0, 0, 3, 5] == math.inf and s[0, 1, 7, 9] == -math.inf
     assert int((~s.isfinite()).sum()) == 2
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,H", [(70, 2), (600, 2)])
+def test_infinite_states_stay_infinite_in_prompts(cuda_lib, T, H, dtype):
+    """An infinity in the state that a prompt starts from, or in the gradient
+    of the one that it leaves, is in the state it leaves, or in the gradient of
+    the one it starts from, and in no other element of either."""
+    t = make(7, (1, T), 1, H, 64, 1, 64, dtype, 1e-3, (0.5, 4.0))
+    t["state"][0, 0, 3, 5], t["state"][0, 1, 7, 9] = math.inf, -math.inf
+    last = prefill(cuda_lib, t)[1]
+    assert last[0, 0, 3, 5] == math.inf and last[0, 1, 7, 9] == -math.inf
+    assert int((~last.isfinite()).sum()) == 2
+    t["state"], t["dlast"] = t["dlast"], t["state"]
+    first = backward(cuda_lib, t)[7]
+    assert first[0, 0, 3, 5] == math.inf and first[0, 1, 7, 9] == -math.inf
+    assert int((~first.isfinite()).sum()) == 2
