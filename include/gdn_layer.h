@@ -143,6 +143,9 @@ gdn_status gdn_scan_backward(const void *x, int64_t x_stride, const void *dt_raw
  *                           scale = amax / 127 (the state codec's).
  * The codes are those of y before any rounding to dt; a zero row or group has
  * scale 0 and codes 0; a row or group that holds a NaN has a NaN scale.
+ * The mean is fp32: a row of which mean(s^2) + eps is 0 there (eps = 0 and
+ * values below 1e-22 at most) has y = 0 and gradients of zero but for
+ * dresidual; one whose squares pass 3e38 has y = 0.
  * d: up to 4096 vectors of 16 bytes, or 8192 elements where pointers, strides
  * or d do not allow vectors; the INT8 groups need them (and d a multiple of
  * the group).

@@ -421,8 +421,8 @@ def gdn_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, qdq: str = 
     and gate share shape and dtype (bf16 or fp32) and may be slices of wider
     rows, also [.., heads, d] slices whose heads are contiguous; weight fp32
     [d].  ``qdq``: "none" returns y in x's dtype, "fp8_row", "int8_g16",
-    "int8_g32" or "int8_g64" a QuantizedRows.  Returns ``(y, s)``, s None
-    without a residual."""
+    "int8_g32" or "int8_g64" a QuantizedRows.  A row of zeros is one of zeros
+    for eps = 0 too.  Returns ``(y, s)``, s None without a residual."""
     dev = _device(x, weight, residual, gate)
     _need(qdq in GDN_NORM_OUT, "qdq must be 'none', 'fp8_row' or 'int8_g16/32/64'")
     _need(x.dim() >= 1 and x.dtype in GDN_DTYPE, "x must be bf16 or fp32 [.., d]")

@@ -34,6 +34,10 @@ struct Rows {
   }
 };
 
+// 1 / sqrt(v), and 0 for v = 0: a row of zeros without an eps has outputs, codes
+// and gradients of zero.
+__device__ __forceinline__ float inverse_root(float v) { return v == 0.0f ? 0.0f : __frsqrt_rn(v); }
+
 // max that keeps a NaN of either side.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -179,7 +183,7 @@ norm_fwd_kernel(const FwdArgs<T> a) {
     for (int v = 0; v < V; ++v) sq = fmaf(f[v], f[v], sq);
   }
   sq = row_sum<TPR>(sq, red);
-  const float r = __frsqrt_rn(sq / (float)a.d + a.eps);
+  const float r = inverse_root(sq / (float)a.d + a.eps);
   const bool wal = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
 
   float y[OUT == kSame ? 1 : VPT][V];
@@ -346,7 +350,7 @@ norm_bwd_kernel(const BwdArgs<T> a) {
         dot += red[turn][1][w0 + i];
       }
     }
-    const float r = __frsqrt_rn(sq / (float)a.d + a.eps);
+    const float r = inverse_root(sq / (float)a.d + a.eps);
     const float c = dot * r * r / (float)a.d;  // ds = r (dn - s c)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
