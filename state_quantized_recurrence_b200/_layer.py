@@ -62,7 +62,8 @@ def _device(*ts) -> int:
 
 def _call(f, name: str, dev: int, stream, *args) -> None:
     """The C call on ``dev`` and on ``stream`` (default: the current stream
-    of ``dev``)."""
+    of ``dev``), which has to be one of ``dev``."""
+    _check_stream(stream, dev)
     if dev == torch.cuda.current_device():
         status = f(*args, _handle(stream, dev))
     else:
@@ -80,6 +81,11 @@ _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _handle(stream, dev: int) -> int:
     return _current_raw(dev) if stream is None else stream.cuda_stream
+
+
+def _check_stream(stream, dev: int) -> None:
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the tensors are on cuda:{dev}")
 
 
 def _ptr(t):
@@ -146,9 +152,7 @@ def _streamed(f):
 
     @functools.wraps(f)
     def call(*args, **kw):
-        if len(args) > at:
-            kw["stream"], args = args[at], args[:at]
-        stream = kw.pop("stream", None) if kw else None
+        stream = args[at] if len(args) > at else kw.get("stream") if kw else None
         if stream is None:
             return f(*args, **kw)
         with torch.cuda.stream(stream):
@@ -323,8 +327,8 @@ def gdn_scan_prefill(x, dt, A, B, C, D=None, dt_bias=None, state_in=None, cu_seq
     n, _ = _sequences(x.shape[:2], cu_seqlens)
     y = torch.empty_like(x)
     state_out = _new((n, x.shape[2], B.shape[-1], x.shape[3]), torch.float32, x, state_in)
-    gdn_scan_prefill_into(x, dt, A, B, C, D, dt_bias, state_in, cu_seqlens, y, state_out,
-                          workspace, stream)
+    gdn_scan_prefill_into.__wrapped__(  # the stream is the current one already
+        x, dt, A, B, C, D, dt_bias, state_in, cu_seqlens, y, state_out, workspace, stream)
     return y, state_out
 
 
