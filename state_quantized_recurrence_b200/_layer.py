@@ -221,6 +221,7 @@ def gdn_conv_prefill(x, weight, bias=None, state_in=None, cu_seqlens=None,
     with int32 ``cu_seqlens``), weight fp32 [C, W] with W = 2, 3 or 4, bias
     fp32 [C], state [n_seq, W - 1, C] (the last inputs, oldest first).  x may
     be a slice of wider rows.  Returns ``(y, state_out)``."""
+    _need(x.dim() == 3 and weight.dim() == 2, "x must be [B, T, C], weight [C, W]")
     n, _ = _sequences(x.shape[:2], cu_seqlens)
     y = torch.empty_like(x)
     state_out = _new((n, weight.shape[-1] - 1, x.shape[-1]), x.dtype, x, state_in)
@@ -324,6 +325,7 @@ def gdn_scan_prefill(x, dt, A, B, C, D=None, dt_bias=None, state_in=None, cu_seq
     int32 ``cu_seqlens``), all bf16 or all fp32 and each possibly a slice of
     wider rows; A, D, dt_bias fp32 [H]; states fp32 [n_seq, H, N, P].
     Returns ``(y, state_out)``."""
+    _need(x.dim() == 4 and B.dim() == 4, "x must be [B, T, H, P], B and C [B, T, G, N]")
     n, _ = _sequences(x.shape[:2], cu_seqlens)
     y = torch.empty_like(x)
     state_out = _new((n, x.shape[2], B.shape[-1], x.shape[3]), torch.float32, x, state_in)

@@ -61,3 +61,26 @@ def test_stream_of_another_device_is_refused(lib, on_device_0, name):  # noqa: F
     """Not dropped for the device's current stream."""
     with pytest.raises(ValueError, match="stream is of cuda:1"):
         calls(lib, stream=OtherStream())[name]()
+
+
+def test_wrong_ranks_are_refused(lib, on_device_0):  # noqa: F811
+    """With a ValueError that says what is wanted, as every other argument."""
+    x, w = torch.zeros(2, 5, 8), torch.zeros(8, 4)
+    q, dt, A, B = torch.zeros(2, 5, 2, 64), torch.zeros(2, 5, 2), torch.zeros(2), \
+        torch.zeros(2, 5, 1, 64)
+    cu = torch.zeros(3, dtype=torch.int32)
+    for f in (lambda: lib.gdn_conv_prefill(x[0], w), lambda: lib.gdn_conv_prefill(x[0, 0], w),
+              lambda: lib.gdn_conv_prefill(x, w[0]), lambda: lib.gdn_conv_prefill(x, w[0, 0]),
+              lambda: lib.gdn_conv_prefill(x[0, 0], w, cu_seqlens=cu),
+              lambda: lib.gdn_conv_decode(x, w, None, x),
+              lambda: lib.gdn_conv_backward(x[0, 0], w, x),
+              lambda: lib.gdn_scan_prefill(q[0], dt[0], A, B[0], B[0]),
+              lambda: lib.gdn_scan_prefill(q[0, 0, 0], dt, A, B, B),
+              lambda: lib.gdn_scan_prefill(q, dt, A, B[0, 0, 0, 0], B),
+              lambda: lib.gdn_scan_prefill(q, dt, A, B, B[0]),
+              lambda: lib.gdn_scan_backward(q[0], dt[0], A, B[0], B[0], q[0]),
+              lambda: lib.gdn_scan_decode(q, dt, A, B, B, q),
+              lambda: lib.gdn_norm(x[0, 0, 0], w[0]),
+              lambda: lib.gdn_norm_backward(x[0, 0, 0], w[0], x[0, 0, 0])):
+        with pytest.raises(ValueError):
+            f()
