@@ -60,3 +60,62 @@ def off(got, want):
     """2-norm of the difference over the 2-norm of what is wanted."""
     want = want.double()
     return float((got.double() - want).norm() / want.norm())
+
+
+# ------------------------------------------------------- pieces of operands ----
+# One sequence whose states tell operands of two bf16 pieces from ones of three,
+# and whose gradients of A tell one from three.  fp32 arithmetic on three pieces: a chunk adds
+# twelve sums in the tensor pipe, which truncates, 2^-24 of a partial sum each
+# on average, which is half of the whole on average; a rounding of the state and
+# one of its decay, and the exponentials of a token (2^-24 on average): 6e-7.
+# Where a state meets an adjoint, the two errors' squares add up, and the sums
+# over the chunk's tokens are twelve truncations more: 1.1e-6.
+STATE_BOUND, DA_BOUND = 1e-6, 1.5e-6
+
+
+def pieces_case():
+    """(x, raw, A, B, C, D, bias, state, dy, dlast); bf16 values where the call's
+    inputs are bf16."""
+    T, H, P, G, N = 1024, 4, 64, 1, 128
+    g = torch.Generator().manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=g)
+    b = lambda *s: r(*s).to(torch.bfloat16)
+    return (b(1, T, H, P), b(1, T, H), -(torch.rand(H, generator=g) * 15 + 1), b(1, T, G, N),
+            b(1, T, G, N), r(H), torch.full((H,), math.log(math.expm1(0.01))), r(1, H, N, P),
+            b(1, T, H, P), r(1, H, N, P))
+
+
+def pieces(t, k):
+    """t as the sum of k bf16 values, each the rounding of what is left."""
+    out, rest = torch.zeros_like(t), t.clone()
+    for _ in range(k):
+        p = rest.float().to(torch.bfloat16).double()
+        out, rest = out + p, rest - p
+    return out
+
+
+def with_pieces(case, k):
+    """(last state, dA) in 64 bits but for operands in k bf16 pieces: w x as it
+    enters the state, states and adjoints as they enter the gradient."""
+    x, raw, A, B, C, _, bias, h, dy, dlast = (t.double() for t in case)
+    v = raw[0] + bias
+    dt = torch.clamp(v, min=0) + torch.log1p(torch.exp(-v.abs()))
+    H = x.shape[2]
+    x, dy, h = x[0], dy[0], h[0]
+    B, C = (t[0].repeat_interleave(H // t.shape[2], 1) for t in (B, C))
+    cuts = [slice(t, t + CHUNK) for t in range(0, x.shape[0], CHUNK)]
+    starts, state = [], h
+    for s in cuts:
+        starts.append(h)
+        h = _one(x[s], dt[s], A, B[s], C[s], h)[1]
+        c = (dt[s] * A).cumsum(0)
+        wx = pieces(x[s] * (torch.exp(c[-1] - c) * dt[s])[..., None], k)
+        state = torch.exp(c[-1])[:, None, None] * state + B[s].permute(1, 2, 0) @ wx.transpose(0, 1)
+    g, dA = dlast[0], 0.0
+    for s, h0 in zip(reversed(cuts), reversed(starts)):
+        a = A.clone().requires_grad_(True)
+        out = _one(x[s], dt[s], a, B[s], C[s], pieces(h0, k))
+        dA = dA + torch.autograd.grad(out, a, [dy[s], pieces(g, k)])[0]
+        h0 = h0.clone().requires_grad_(True)
+        g = torch.autograd.grad(_one(x[s], dt[s], A, B[s], C[s], h0), h0, [dy[s], g])[0]
+    return state[None], dA

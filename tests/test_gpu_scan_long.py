@@ -143,3 +143,66 @@ def test_infinite_states_stay_infinite_in_prompts(cuda_lib, T, H, dtype):
     first = backward(cuda_lib, t)[7]
     assert first[0, 0, 3, 5] == math.inf and first[0, 1, 7, 9] == -math.inf
     assert int((~first.isfinite()).sum()) == 2
+
+
+FORMS = [  # tokens or packed lengths, sequences, heads, P, G, N, cut into runs
+    (5000, 1, 1, 64, 1, 64, True),                        # 20 runs of a sequence
+    ((3000, 0, 700, 64, 1, 1500), 6, 2, 64, 1, 128, True),   # packed, and cut
+    (2210, 2, 12, 128, 2, 128, True),                     # six heads a CTA of the gradient
+    (1150, 2, 12, 64, 2, 64, True),                       # three, two CTAs a group
+    ((1000, 0, 4000, 33, 65), 5, 8, 64, 1, 128, True),    # eight, packed
+    (700, 4, 32, 64, 4, 64, False),                       # not cut: 128 units
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", FORMS, ids=[str(i) for i in range(len(FORMS))])
+def test_runs_heads_and_packed_sequences(cuda_lib, case, dtype):
+    """Every output and gradient in the forms that long calls and many heads
+    take.  bf16: M and W as in test_gradients_summed_over_many_heads; states
+    and sums over all tokens within the bound of test_states_of_long_prompts,
+    twice where a state meets an adjoint.  fp32: the state is rounded T times,
+    as in test_a_state_that_forgets_almost_nothing.  ddt is the sum of A l and
+    x . du, which can cancel: four times the bound of its terms."""
+    T, n, H, P, G, N, cut = case
+    cu, lead = None, (n, T)
+    if not isinstance(T, int):
+        cu, lead = [0], (1, sum(T))
+        for v in T:
+            cu.append(cu[-1] + v)
+        T = max(T)
+    bytes_ = cuda_lib.lib.gdn_scan_prefill_workspace_bytes(
+        n, lead[1], H, P, G, N, cuda_lib.GDN_DTYPE[dtype], int(cu is not None))
+    assert (bytes_ > 0) == cut
+    t = make(8, lead, n, H, P, G, N, dtype, 0.01, (1.0, 16.0))
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    got = prefill(cuda_lib, t, cud) + backward(cuda_lib, t, cud)
+    cuda_lib.check_last_error()
+    want = long.scan_grad(*args(t, cu), t["dy"], t["dlast"])
+    if dtype == BF16:
+        state = (12 * 2.0 + 1) * 2.0 ** -24 + math.sqrt(T / 64) * 2.0 ** -24 + 2.0 ** -21
+        pair, sums, step = (rounding(2.0 ** -k) for k in (18, 20, 18))
+    else:
+        state = pair = math.sqrt(T) * 2.0 ** -25 + 2.0 ** -21
+        sums, step = 2 * state, 4 * state
+    bounds = (("y", pair), ("state_out", state), ("dx", 2 * pair), ("ddt", 2 * step),
+              ("dA", 2 * state), ("dB", sums), ("dC", sums), ("dD", state),
+              ("ddt_bias", 2 * state), ("dstate_in", state))
+    for (name, bound), a, b in zip(bounds, got, want):
+        assert long.off(a, b.to(a.dtype)) <= bound, name
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_operands_of_three_pieces(cuda_lib, dtype):
+    """Sums over all tokens stay fp32 quantities: bounds that operands of fewer
+    bf16 pieces are beyond (``test_layer_long.py``)."""
+    x, raw, A, B, C, D, bias, h, dy, dl = (t.cuda() for t in long.pieces_case())
+    t = dict(x=x.to(dtype), raw=raw.to(dtype), A=A, B=B.to(dtype), C=C.to(dtype), D=D, bias=bias,
+             state=h, dy=dy.to(dtype), dlast=dl)
+    want = long.scan_grad(*args(t), t["dy"], t["dlast"])
+    last, got = prefill(cuda_lib, t)[1], backward(cuda_lib, t)
+    assert long.off(last, want[1]) <= long.STATE_BOUND
+    assert long.off(got[7], want[9]) <= long.STATE_BOUND
+    assert long.off(got[2], want[4]) <= long.DA_BOUND
+    assert long.off(got[6], want[8]) <= long.DA_BOUND
+    assert long.off(got[5], want[7]) <= long.STATE_BOUND

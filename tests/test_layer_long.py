@@ -22,3 +22,20 @@ def test_chunks_are_the_tokens(lens):
     dy, dl = r(*lead, H, P), r(n, H, N, P)
     for a, b in zip(long.scan_grad(*args, dy, dl), ref.scan(*args, dy, dl)):
         assert (a - b).abs().max() <= 1e-11 * b.abs().max()
+
+
+def test_bounds_tell_pieces_apart():
+    """The bounds that the library's states and gradients of A are held to:
+    operands of one bf16 piece are far beyond them, ones of three far within.  A
+    state of two is beyond as well; a gradient of A of two need not be, whose
+    errors have random signs and average out over the tokens (5e-7 here)."""
+    case = long.pieces_case()
+    x, raw, A, B, C, D, bias, h, dy, dl = (t.double() for t in case)
+    want = long.scan_grad(x, raw, A, B, C, D, bias, h, None, dy, dl)
+    off = {}
+    for k in (1, 2, 3):
+        state, dA = long.with_pieces(case, k)
+        off[k] = long.off(state, want[1]), long.off(dA, want[4])
+    assert off[1][0] > 100 * long.STATE_BOUND and off[1][1] > 100 * long.DA_BOUND
+    assert off[2][0] > 2 * long.STATE_BOUND
+    assert off[3][0] < long.STATE_BOUND / 20 and off[3][1] < long.DA_BOUND / 20
