@@ -55,25 +55,34 @@ unsigned units(const Call &c) { return (unsigned)(c.n_seq * c.H * (c.P / 64)); }
 // Sequences are cut into runs of chunks where (sequence, head, 64 columns)
 // units alone would leave SMs idle: a first launch forms what each run adds
 // to a zero state, a second turns that into the state each run starts from.
-// That is half as much work again, so a call with 100 units or more goes
-// without (4 x 4096 tokens x 16 heads of 128, 128 units: 281 us, against 337
-// cut into three and 332 into nine); below, there are as many runs as two
-// CTAs on every SM, of four chunks at least (one sequence of 8191 tokens, 8
-// units: 61 us; 80 with half as many).
+// That is half of a prompt's work again, and twice a gradient's sweeps; there
+// are as many runs as two CTAs on every SM, of four chunks at least (one
+// sequence of 8191 tokens, 8 units: 61 us; 80 with half as many).  `enough`
+// units go without.  Measured, us cut / not cut, one sequence of N = 128:
+//   units                       8         32         56          72         96        112
+//   bf16 prompt, 4096      41 / 282   90 / 283  171 / 285   205 / 285  256 / 289  333 / 290
+//   fp32 prompt, 2048     201 / 743  278 / 747  507 / 754   641 / 794  834 / 911  1003 / 914
+//   bf16 gradient, 4096   118 / 281  375 / 451  635 / 619   759 / 703  1007 / 959  1173 / 1054
+//   fp32 gradient, 2048   324 / 823  1064 / 1454  1860 / 1940  2322 / 2190  3043 / 2736  3624 / 3045
+// Shorter sequences lie closer together: bf16 prompts of 1024 tokens 59 / 76 at
+// 56 units and 78 / 76 at 96, gradients 120 / 127 at 32 and 195 / 176 at 56, fp32
+// calls of 512 tokens 5 % slower cut at 32.  The packed rule goes by the mean
+// length: one long sequence among many of a chunk or two (a mean of four
+// chunks at most), or in a call of enough units, is not cut.
 struct Plan {
   int seg_chunks;   // chunks of a run
   bool split;
   long long slots;  // run slots of the call
   size_t state, decay, bytes;  // workspace parts
 };
-constexpr int kResident = 2 * 148, kEnough = 100;
-Plan plan(int n_seq, int T, int H, int P, int N, bool packed) {
+constexpr int kResident = 2 * 148, kEnough = 100, kEnoughGrad = 50;
+Plan plan(int n_seq, int T, int H, int P, int N, bool packed, int enough) {
   Plan p = {};
   const long long units = (long long)n_seq * H * (P / 64);
   const long long chunks = (T + 63LL) / 64;
   const long long mean = packed && n_seq > 0 ? (chunks + n_seq - 1) / n_seq : chunks;
   long long seg = chunks > 0 ? chunks : 1;
-  if (units > 0 && units < kEnough && mean > 4) {
+  if (units > 0 && units < enough && mean > 4) {
     const long long want = (kResident + units - 1) / units;
     long long s = (mean + want - 1) / want;
     if (s < 4) s = 4;
@@ -120,7 +129,7 @@ Ends ends_at(char *ws, size_t state, size_t decay) {
 template <typename T, int N>
 gdn_status prefill_typed(const Call &c, char *ws, void *y, float *state_out, unsigned *err, cudaStream_t st) {
   const In<T> in = typed<T>(c);
-  const Plan p = plan(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr);
+  const Plan p = plan(c.n_seq, c.T, c.H, c.P, c.N, c.cu != nullptr, kEnough);
   Ends ends{nullptr, nullptr};
   if (p.split) {
     ends = ends_at(ws, p.state, p.decay);
@@ -171,7 +180,14 @@ struct Workspace {
 
 // CTAs that a group's heads are split over: each share forms C B^T again
 // (half a head's work), so the split is the one with the least work in a
-// row on one of the 148 SMs.
+// row on one of the 148 SMs.  The whole gradient in us, P = 64, N = 128, with the
+// split chosen here starred:
+//   shares              1     2     3     4     8    16
+//   8 chunks, R = 16   252   148   123    96    73   *62
+//   16 chunks          254   152   125    98   *74    82
+//   64 chunks          314  *214   244   217   233   248
+//   128 chunks        *376   387   418   395   398   458
+//   256 chunks, R = 32 1202  1222  1226 *1137  1194  1295
 int head_splits(long long chunks_groups, int R) {
   int best = 1;
   double least = 1e30;
@@ -200,7 +216,7 @@ Workspace workspace(int n_seq, int T, int H, int P, int G, int N, gdn_dtype dt, 
   w.dC = w.dB + sums;
   w.part = w.dC + sums;
   w.bytes = w.part + (size_t)w.slots * H * 16;
-  w.runs = plan(n_seq, T, H, P, N, packed);
+  w.runs = plan(n_seq, T, H, P, N, packed, kEnoughGrad);
   if (w.runs.split) {
     w.fwd = w.bytes;
     w.fwd_decay = w.fwd + w.runs.decay;
@@ -315,7 +331,7 @@ size_t gdn_scan_prefill_workspace_bytes(int n_seq, int T, int H, int P, int G, i
   const scan::Call c{nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, nullptr, nullptr, nullptr,
                      nullptr, nullptr, 0, T, H, P, G, N};
   if (n_seq <= 0 || scan::check(c, dtype, false) != GDN_OK) return 0;
-  return scan::plan(n_seq, T, H, P, N, packed != 0).bytes;
+  return scan::plan(n_seq, T, H, P, N, packed != 0, scan::kEnough).bytes;
 }
 
 gdn_status gdn_scan_prefill(const void *x, int64_t x_stride, const void *dt_raw,

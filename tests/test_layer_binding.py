@@ -84,3 +84,17 @@ def test_wrong_ranks_are_refused(lib, on_device_0):  # noqa: F811
               lambda: lib.gdn_norm_backward(x[0, 0, 0], w[0], x[0, 0, 0])):
         with pytest.raises(ValueError):
             f()
+
+
+def test_scan_runs_by_units(lib):  # noqa: F811
+    """Prompts are cut into runs below 100 units, gradients below 50 (either
+    side measured beside the rule); a gradient that is not cut has room for
+    the chunks' states and adjoints and the heads' sums alone."""
+    T, P, N = 4096, 64, 128
+    chunks, state = T // 64, N * P * 4
+    for H in (1, 48, 49, 50, 64, 99, 100, 128):
+        prompt = lib.lib.gdn_scan_prefill_workspace_bytes(1, T, H, P, H, N, 1, 0)
+        assert (prompt > 0) == (H < 100)
+        grad = lib.lib.gdn_scan_backward_workspace_bytes(1, T, H, P, H, N, 1, 0)
+        whole = 2 * chunks * H * state + 2 * T * H * N * 4 + chunks * H * 16
+        assert (grad > whole) == (H < 50) and (H < 50 or grad == whole)
