@@ -479,12 +479,18 @@ gdn_status fwd_launch(const Args &a, void *y, void *so, unsigned *err, cudaStrea
 
 template <typename T, int V, int W, bool SILU>
 gdn_status fwd_run(const Args &a, void *y, void *so, unsigned *err, cudaStream_t st) {
-  // Runs of 32 tokens re-read 3 rows in 32; a call too small to give every
-  // SM two such CTAs takes runs of 8, which spreads it over four times as many.
-  const long long cb = (a.C + 32LL * V - 1) / (32 * V);
-  if (slot_count(a.n_seq, a.T, kRun * kWarps, a.cu != nullptr) * cb < 2 * 148)
-    return fwd_launch<T, V, W, SILU, kRunShort>(a, y, so, err, st);
-  return fwd_launch<T, V, W, SILU, kRun>(a, y, so, err, st);
+  // Runs of 32 tokens re-read 3 rows in 32, runs of 8 spread a call over four
+  // times as many CTAs.  bf16, us with runs of 8 / 32 by CTAs of the latter:
+  // 5.1 / 7.2 at 64, 7.7 / 7.2 at 144, 9.2 / 9.8 at 204, 9.6 / 9.8 at 216,
+  // 12.2 / 9.8 at 272, 20.5 / 15.9 at 544, 49 / 34 at 1088.  fp32 calls
+  // were faster with runs of 8 at every size (6.7 / 13.3 at 64, 19 / 25 at 272,
+  // 75 / 108 at 1088) and always take them.
+  if constexpr (sizeof(T) == 2) {
+    const long long cb = (a.C + 32LL * V - 1) / (32 * V);
+    if (slot_count(a.n_seq, a.T, kRun * kWarps, a.cu != nullptr) * cb >= 148 * 3 / 2)
+      return fwd_launch<T, V, W, SILU, kRun>(a, y, so, err, st);
+  }
+  return fwd_launch<T, V, W, SILU, kRunShort>(a, y, so, err, st);
 }
 
 template <typename T, int V, int W, bool SILU>

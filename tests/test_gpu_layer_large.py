@@ -30,7 +30,8 @@ def conv_ctas(T, n, C, dtype):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("case", CONV, ids=[str(i) for i in range(len(CONV))])
 def test_convolution_in_long_runs(cuda_lib, case, dtype):
-    """Two CTAs on every SM and more: runs of 32 tokens."""
+    """Enough CTAs for runs of 32 tokens (bf16; fp32 takes runs of 8, here of
+    more tiles than in ``test_gpu_conv.py``)."""
     T, n, C, W, pad, state = case
     assert conv_ctas(T, n, C, dtype) >= 2 * SMS
     cu = None if isinstance(T, int) else cu_of(T)
