@@ -499,8 +499,12 @@ gdn_status decode_run(const Args &a, void *state, void *y, cudaStream_t st) {
   const int threads = nv >= 128 ? 128 : (int)((nv + 31) / 32 * 32);
   const long long cb = (nv + threads - 1) / threads;
   if (cb > 65535) return GDN_ERR_UNSUPPORTED;
-  // four sequences a thread where that still leaves every SM a CTA
-  if (a.n_seq * cb >= 4 * 148)
+  // Four sequences a thread once one would make this many CTAs.  us of a call
+  // in a row of them, one / four, by the CTAs of one: bf16 2.26 / 2.77 at 192,
+  // 2.87 / 2.87 at 288, 3.18 / 2.77 at 320, 3.81 / 2.87 at 480, 6.87 / 4.71 at 1280;
+  // fp32 2.36 / 3.08 at 288, 2.98 / 3.28 at 640, 3.57 / 3.69 at 960, 4.00 / 3.70 at
+  // 1152, 6.26 / 5.13 at 2304.
+  if (a.n_seq * cb >= (sizeof(T) == 2 ? 2 : 7) * 148)
     conv_decode_kernel<T, V, W, SILU, 4><<<dim3((unsigned)((a.n_seq + 3LL) / 4), (unsigned)cb), threads, 0, st>>>(
         static_cast<const T *>(a.x), a.xs, a.w, a.b, static_cast<T *>(state), a.n_seq, a.C,
         static_cast<T *>(y));
