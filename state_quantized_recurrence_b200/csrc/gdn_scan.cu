@@ -114,7 +114,7 @@ gdn_status run_starts(const Call &c, const Plan &p, const T *dy, const float *ds
     if (!allow_smem(ends_mma_kernel<N>, smem, done)) return GDN_ERR_CUDA;
     ends_mma_kernel<N><<<grid, kSweepThreads, smem, st>>>(in, dy, p.seg_chunks, fwd, rev, err);
   } else {
-    adds_kernel<T, N><<<grid, 256, 0, st>>>(in, dy, p.seg_chunks, fwd, rev, err);
+    adds_kernel<N><<<grid, 256, 0, st>>>(in, dy, p.seg_chunks, fwd, rev, err);
   }
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   const long long np = (long long)c.N * c.P;
@@ -143,7 +143,7 @@ gdn_status prefill_typed(const Call &c, char *ws, void *y, float *state_out, uns
     scan_mma_kernel<N><<<run_blocks(c, p), kSweepThreads, smem, st>>>(in, p.seg_chunks, ends,
                                                                       static_cast<T *>(y), state_out, err);
   } else {
-    forward_kernel<T, N><<<run_blocks(c, p), 256, 0, st>>>(in, p.seg_chunks, ends, static_cast<T *>(y),
+    forward_kernel<N><<<run_blocks(c, p), 256, 0, st>>>(in, p.seg_chunks, ends, static_cast<T *>(y),
                                                            state_out, err);
   }
   return launched();
@@ -264,10 +264,10 @@ gdn_status backward_f32(const Call &c, const Grads &g, char *ws, unsigned *err, 
     rev = ends_at(ws, w.rev, w.rev_decay);
     if ((s = run_starts<float, N>(c, w.runs, dy, g.dstate_out, fwd, rev, err, st)) != GDN_OK) return s;
   }
-  boundaries_kernel<float, N><<<dim3(run_blocks(c, w.runs), 2), 256, 0, st>>>(
+  boundaries_kernel<N><<<dim3(run_blocks(c, w.runs), 2), 256, 0, st>>>(
       in, dy, g.dstate_out, w.runs.seg_chunks, fwd, rev, states, adjoints, g.dstate_in, err);
   if ((s = launched()) != GDN_OK) return s;
-  auto kern = chunk_grad_kernel<float, N, P>;
+  auto kern = chunk_grad_kernel<N, P>;
   constexpr size_t smem = ChunkLayout<N, P>::bytes;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, (int)smem, done)) return GDN_ERR_CUDA;

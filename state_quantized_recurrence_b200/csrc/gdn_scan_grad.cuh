@@ -133,7 +133,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
   const bool lower = sc <= sr;
   const int gr = 16 * (warp >> 2), gc = (N / 4) * (warp & 3);  // rows, columns of dB and dC
   const int ur = gr, uc = 16 * (warp & 3);                     // of du
-  float S[2][4], aB[1][2 * kJ][4], aC[1][2 * kJ][4];
+  float S[2][4], aB[2 * kJ][4], aC[2 * kJ][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -141,7 +141,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
 #pragma unroll
   for (int j = 0; j < 2 * kJ; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) aB[0][j][e] = aC[0][j][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) aB[j][e] = aC[j][e] = 0.0f;
 
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
@@ -249,7 +249,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
           }
         }
       }
-      float(&acc)[2 * kJ][4] = side ? aB[0] : aC[0];
+      float(&acc)[2 * kJ][4] = side ? aB : aC;
 #pragma unroll
       for (int j = 0; j < 2 * kJ; ++j)
 #pragma unroll
@@ -309,7 +309,7 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
           bf2_get(o, oa, ob);
           const float ta = T[j][2 * e], tb = T[j][2 * e + 1];
           s = fmaf(oa, ta, fmaf(ob, tb, s));
-          float(&acc)[4] = side ? aB[0][j] : aC[0][j];
+          float(&acc)[4] = side ? aB[j] : aC[j];
           acc[2 * e] = fmaf(f, ta, acc[2 * e]);
           acc[2 * e + 1] = fmaf(f, tb, acc[2 * e + 1]);
         }
@@ -338,64 +338,53 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
       with_state(1, tX, sG, 2);
       // du = M^T dy + e^{c_n - c_j} B G^T and dx
       {
-        float U[1][2][4], T[1][2][4];
+        float U[2][4], T[2][4];
 #pragma unroll
-        for (int i = 0; i < 1; ++i)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) U[i][j][e] = T[i][j][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) U[j][e] = T[j][e] = 0.0f;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (kk < ur / 16) continue;  // above the diagonal
           uint32_t b[4];
           ldsm4t(block_rows<64>(tY, 16 * kk, uc / 8, lane), b);
 #pragma unroll
-          for (int i = 0; i < 1; ++i) {
-#pragma unroll
-            for (int piece = 0; piece < 2; ++piece) {
-              uint32_t a[4];
-              ldsm4t(block_cols<64>(sM + piece * kTileBytes<64>, 16 * kk, (ur + 16 * i) / 8, lane), a);
-              mma16816(U[i][0], a, b[0], b[1]);
-              mma16816(U[i][1], a, b[2], b[3]);
-            }
+          for (int piece = 0; piece < 2; ++piece) {
+            uint32_t a[4];
+            ldsm4t(block_cols<64>(sM + piece * kTileBytes<64>, 16 * kk, ur / 8, lane), a);
+            mma16816(U[0], a, b[0], b[1]);
+            mma16816(U[1], a, b[2], b[3]);
           }
         }
 #pragma unroll
         for (int kk = 0; kk < N / 16; ++kk) {
-          uint32_t a[1][4];
-#pragma unroll
-          for (int i = 0; i < 1; ++i) ldsm4(block_rows<N>(sB, ur + 16 * i, 2 * kk, lane), a[i]);
+          uint32_t a[4];
+          ldsm4(block_rows<N>(sB, ur, 2 * kk, lane), a);
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece) {
             uint32_t b[4];
             ldsm4(block_cols<N>(sG + piece * kTileBytes<N>, uc, 2 * kk, lane), b);
-#pragma unroll
-            for (int i = 0; i < 1; ++i) {
-              mma16816(T[i][0], a[i], b[0], b[1]);
-              mma16816(T[i][1], a[i], b[2], b[3]);
-            }
+            mma16816(T[0], a, b[0], b[1]);
+            mma16816(T[1], a, b[2], b[3]);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 1; ++i)
+        for (int e = 0; e < 2; ++e) {
+          const int r = ur + g + 8 * e;
+          const float d = m.del[r], dt = m.dt[r];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = ur + 16 * i + g + 8 * e;
-            const float d = m.del[r], dt = m.dt[r];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t yr;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(yr) : "r"(tile_at<64>(tY, r, uc / 8 + j) + q * 4));
-              float ya, yb;
-              bf2_get(yr, ya, yb);
-              const float ua = fmaf(d, T[i][j][2 * e], U[i][j][2 * e]);
-              const float ub = fmaf(d, T[i][j][2 * e + 1], U[i][j][2 * e + 1]);
-              if (r < n)
-                *reinterpret_cast<uint32_t *>(dx + ((row0 + r) * in.H + h) * P + pt * 64 + uc + 8 * j + 2 * q) =
-                    bf2_set(fmaf(dt, ua, Dh * ya), fmaf(dt, ub, Dh * yb));
-            }
+          for (int j = 0; j < 2; ++j) {
+            uint32_t yr;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(yr) : "r"(tile_at<64>(tY, r, uc / 8 + j) + q * 4));
+            float ya, yb;
+            bf2_get(yr, ya, yb);
+            const float ua = fmaf(d, T[j][2 * e], U[j][2 * e]);
+            const float ub = fmaf(d, T[j][2 * e + 1], U[j][2 * e + 1]);
+            if (r < n)
+              *reinterpret_cast<uint32_t *>(dx + ((row0 + r) * in.H + h) * P + pt * 64 + uc + 8 * j + 2 * q) =
+                  bf2_set(fmaf(dt, ua, Dh * ya), fmaf(dt, ub, Dh * yb));
           }
+        }
       }
       copy_wait<0>();
       __syncthreads();  // the third pieces are there
@@ -488,25 +477,23 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
     }
   }
 #pragma unroll
-  for (int i = 0; i < 1; ++i)
+  for (int e = 0; e < 2; ++e) {
+    const int r = gr + g + 8 * e;
+    if (r >= n) continue;
+    const long long row = (row0 + r) * in.G + grp;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = gr + 16 * i + g + 8 * e;
-      if (r >= n) continue;
-      const long long row = (row0 + r) * in.G + grp;
-#pragma unroll
-      for (int j = 0; j < 2 * kJ; ++j) {
-        const int c = gc + 8 * j + 2 * q;
-        if (splits == 1) {
-          *reinterpret_cast<uint32_t *>(out.b + row * N + c) = bf2_set(aB[i][j][2 * e], aB[i][j][2 * e + 1]);
-          *reinterpret_cast<uint32_t *>(out.c + row * N + c) = bf2_set(aC[i][j][2 * e], aC[i][j][2 * e + 1]);
-        } else {
-          const long long at = (row * splits + sp) * N + c;
-          *reinterpret_cast<float2 *>(out.pb + at) = make_float2(aB[i][j][2 * e], aB[i][j][2 * e + 1]);
-          *reinterpret_cast<float2 *>(out.pc + at) = make_float2(aC[i][j][2 * e], aC[i][j][2 * e + 1]);
-        }
+    for (int j = 0; j < 2 * kJ; ++j) {
+      const int c = gc + 8 * j + 2 * q;
+      if (splits == 1) {
+        *reinterpret_cast<uint32_t *>(out.b + row * N + c) = bf2_set(aB[j][2 * e], aB[j][2 * e + 1]);
+        *reinterpret_cast<uint32_t *>(out.c + row * N + c) = bf2_set(aC[j][2 * e], aC[j][2 * e + 1]);
+      } else {
+        const long long at = (row * splits + sp) * N + c;
+        *reinterpret_cast<float2 *>(out.pb + at) = make_float2(aB[j][2 * e], aB[j][2 * e + 1]);
+        *reinterpret_cast<float2 *>(out.pc + at) = make_float2(aC[j][2 * e], aC[j][2 * e + 1]);
       }
     }
+  }
 }
 
 }  // namespace scan

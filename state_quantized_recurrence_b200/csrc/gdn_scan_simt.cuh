@@ -1,9 +1,11 @@
-// Selective state space scan on the CUDA cores, for every type and shape:
+// Selective state space scan on the CUDA cores, fp32 prompts and gradients and
+// single tokens of either type:
 //   S_t = a_t S_{t-1} + B_t u_t^T,  y_t = S_t^T C_t + D x_t,
 //   a_t = exp(dt_t A), u_t = dt_t x_t, dt_t = softplus(raw_t + bias)
 // token by token with the state in registers (forward, and the states and
 // their adjoints at chunk boundaries for the gradient), and the gradient of
-// one 64-token chunk in matrix form.
+// one 64-token chunk in matrix form.  What bf16 calls share is here too: their
+// arguments, the starts of runs, and the sums over heads and chunks.
 #pragma once
 
 #include "gdn_layer.cuh"
@@ -140,9 +142,9 @@ start_states_kernel(const int *__restrict__ cu, int n_seq, int T, int H, long lo
 enum Sweep : int { kForward = 0, kStates = 1, kAdjoint = 2, kAdds = 3, kAddsBack = 4 };
 constexpr int kTok = 16;  // tokens staged at a time
 
-template <typename T, int N, int MODE>
-__device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy, const float *first,
-                                      int seg_chunks, Ends ends, T *__restrict__ y, float *out_state,
+template <int N, int MODE>
+__device__ __forceinline__ void sweep(const In<float> &in, const float *__restrict__ dy, const float *first,
+                                      int seg_chunks, Ends ends, float *__restrict__ y, float *out_state,
                                       float *__restrict__ dump, unsigned *err) {
   constexpr int R = N / 4;
   constexpr bool kBack = MODE == kAdjoint || MODE == kAddsBack, kAdd = MODE == kAdds || MODE == kAddsBack;
@@ -181,11 +183,11 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
     __syncthreads();
     for (int i = tid; i < n * N; i += 256) {
       const long long row = t0 + b0 + i / N;
-      if (!kBack) sb[i / N][i % N] = to_f32(in.B[row * in.bs + g * N + i % N]);
-      if (kBack || MODE == kForward) sc[i / N][i % N] = to_f32(in.C[row * in.cs + g * N + i % N]);
+      if (!kBack) sb[i / N][i % N] = in.B[row * in.bs + g * N + i % N];
+      if (kBack || MODE == kForward) sc[i / N][i % N] = in.C[row * in.cs + g * N + i % N];
     }
     if (tid < n) {
-      const float dt = softplus(to_f32(in.raw[(t0 + b0 + tid) * in.rs + h]) + bias);
+      const float dt = softplus(in.raw[(t0 + b0 + tid) * in.rs + h] + bias);
       sdt[tid] = dt;
       // The decay as two floats: its rounding alone, multiplied up over a few
       // hundred tokens, costs a slowly forgetting state 1e-6 (and without the
@@ -201,7 +203,7 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
     for (int i = tid; i < n * 64; i += 256) {
       const long long row = t0 + b0 + i / 64;
       const long long c = (long long)h * in.P + pt * 64 + i % 64;
-      su[i / 64][i % 64] = to_f32(kBack ? dy[row * in.H * in.P + c] : in.x[row * in.xs + c]);
+      su[i / 64][i % 64] = kBack ? dy[row * in.H * in.P + c] : in.x[row * in.xs + c];
     }
     __syncthreads();
     if constexpr (kBack) {
@@ -254,7 +256,7 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
         for (int i = tid; i < n * 64; i += 256) {
           const int t = i / 64, c = i % 64;
           const float o = (sy[0][t][c] + sy[1][t][c]) + (sy[2][t][c] + sy[3][t][c]) + D * su[t][c];
-          y[((t0 + b0 + t) * in.H + h) * in.P + pt * 64 + c] = T(o);
+          y[((t0 + b0 + t) * in.H + h) * in.P + pt * 64 + c] = o;
         }
       }
     }
@@ -276,28 +278,28 @@ __device__ __forceinline__ void sweep(const In<T> &in, const T *__restrict__ dy,
   }
 }
 
-template <typename T, int N>
+template <int N>
 __global__ void __launch_bounds__(256)
-forward_kernel(const In<T> in, int seg_chunks, Ends ends, T *__restrict__ y, float *out_state, unsigned *err) {
-  sweep<T, N, kForward>(in, nullptr, in.state_in, seg_chunks, ends, y, out_state, nullptr, err);
+forward_kernel(const In<float> in, int seg_chunks, Ends ends, float *__restrict__ y, float *out_state, unsigned *err) {
+  sweep<N, kForward>(in, nullptr, in.state_in, seg_chunks, ends, y, out_state, nullptr, err);
 }
-template <typename T, int N>
+template <int N>
 __global__ void __launch_bounds__(256)
-adds_kernel(const In<T> in, const T *__restrict__ dy, int seg_chunks, Ends fwd, Ends rev, unsigned *err) {
-  if (blockIdx.y == 0) sweep<T, N, kAdds>(in, nullptr, nullptr, seg_chunks, fwd, nullptr, nullptr, nullptr, err);
-  else sweep<T, N, kAddsBack>(in, dy, nullptr, seg_chunks, rev, nullptr, nullptr, nullptr, err);
+adds_kernel(const In<float> in, const float *__restrict__ dy, int seg_chunks, Ends fwd, Ends rev, unsigned *err) {
+  if (blockIdx.y == 0) sweep<N, kAdds>(in, nullptr, nullptr, seg_chunks, fwd, nullptr, nullptr, nullptr, err);
+  else sweep<N, kAddsBack>(in, dy, nullptr, seg_chunks, rev, nullptr, nullptr, nullptr, err);
 }
 // The gradient's two sweeps, side by side: a sweep is a chain of tokens that
 // leaves most of an SM idle.
-template <typename T, int N>
+template <int N>
 __global__ void __launch_bounds__(256)
-boundaries_kernel(const In<T> in, const T *__restrict__ dy, const float *__restrict__ dstate_out,
+boundaries_kernel(const In<float> in, const float *__restrict__ dy, const float *__restrict__ dstate_out,
                   int seg_chunks, Ends fwd, Ends rev, float *__restrict__ states,
                   float *__restrict__ adjoints, float *dstate_in, unsigned *err) {
   if (blockIdx.y == 0)
-    sweep<T, N, kStates>(in, nullptr, in.state_in, seg_chunks, fwd, nullptr, nullptr, states, err);
+    sweep<N, kStates>(in, nullptr, in.state_in, seg_chunks, fwd, nullptr, nullptr, states, err);
   else
-    sweep<T, N, kAdjoint>(in, dy, dstate_out, seg_chunks, rev, nullptr, dstate_in, adjoints, err);
+    sweep<N, kAdjoint>(in, dy, dstate_out, seg_chunks, rev, nullptr, dstate_in, adjoints, err);
 }
 
 // One decode token of one (sequence, head, 64-column tile).  Bound by the
@@ -384,8 +386,7 @@ __device__ __forceinline__ float exp_gap(const ChunkSmem &m, int i, int j) {
 // dt, its sigmoid and the decay sums of a chunk's n tokens, by one warp (two
 // tokens a lane).  The sums are formed in 64 bits and kept as two floats:
 // differences of neighbours stay exact where the sums themselves are large.
-template <typename T>
-__device__ __forceinline__ void chunk_decays(const In<T> &in, long long row0, int n, int h,
+__device__ __forceinline__ void chunk_decays(const In<float> &in, long long row0, int n, int h,
                                              float A, float bias, ChunkSmem &m) {
   const int lane = threadIdx.x & 31;
   double a[2];
@@ -394,7 +395,7 @@ __device__ __forceinline__ void chunk_decays(const In<T> &in, long long row0, in
     const int t = 2 * lane + k;
     float dt = 0.0f, sg = 0.0f;
     if (t < n) {
-      const float v = to_f32(in.raw[(row0 + t) * in.rs + h]) + bias;
+      const float v = in.raw[(row0 + t) * in.rs + h] + bias;
       dt = softplus(v);
       sg = 1.0f / (1.0f + expf(-v));
     }
@@ -455,10 +456,10 @@ __device__ __forceinline__ void stage_columns(const float *__restrict__ state, i
   __syncthreads();
 }
 
-template <typename T, int N, int P>
+template <int N, int P>
 __global__ void __launch_bounds__(256)
-chunk_grad_kernel(const In<T> in, const T *__restrict__ dy, const float *__restrict__ states,
-                  const float *__restrict__ adjoints, T *__restrict__ dx, T *__restrict__ draw,
+chunk_grad_kernel(const In<float> in, const float *__restrict__ dy, const float *__restrict__ states,
+                  const float *__restrict__ adjoints, float *__restrict__ dx, float *__restrict__ draw,
                   float *__restrict__ dBh, float *__restrict__ dCh, float *__restrict__ part) {
   using L = ChunkLayout<N, P>;
   extern __shared__ __align__(16) float sm[];
@@ -479,13 +480,13 @@ chunk_grad_kernel(const In<T> in, const T *__restrict__ dy, const float *__restr
   const float A = in.A[h], D = in.D ? in.D[h] : 0.0f, bias = in.bias ? in.bias[h] : 0.0f;
   for (int i = tid; i < kChunk * N; i += 256) {
     const int r = i / N, c = i % N;
-    sB[r * L::bn + c] = r < n ? to_f32(in.B[(row0 + r) * in.bs + g * N + c]) : 0.0f;
-    sC[r * L::bn + c] = r < n ? to_f32(in.C[(row0 + r) * in.cs + g * N + c]) : 0.0f;
+    sB[r * L::bn + c] = r < n ? in.B[(row0 + r) * in.bs + g * N + c] : 0.0f;
+    sC[r * L::bn + c] = r < n ? in.C[(row0 + r) * in.cs + g * N + c] : 0.0f;
   }
   for (int i = tid; i < kChunk * P; i += 256) {
     const int r = i / P, c = i % P;
-    sX[r * L::bp + c] = r < n ? to_f32(in.x[(row0 + r) * in.xs + (long long)h * P + c]) : 0.0f;
-    sY[r * L::bp + c] = r < n ? to_f32(dy[((row0 + r) * in.H + h) * P + c]) : 0.0f;
+    sX[r * L::bp + c] = r < n ? in.x[(row0 + r) * in.xs + (long long)h * P + c] : 0.0f;
+    sY[r * L::bp + c] = r < n ? dy[((row0 + r) * in.H + h) * P + c] : 0.0f;
   }
   if (tid < 32) chunk_decays(in, row0, n, h, A, bias, m);
   __syncthreads();
@@ -574,7 +575,7 @@ chunk_grad_kernel(const In<T> in, const T *__restrict__ dy, const float *__restr
         xdu = fmaf(xv, du, xdu);
         qq = fmaf(xv, far, qq);
         dD = fmaf(xv, dv, dD);
-        if (r < n) dx[((row0 + r) * in.H + h) * P + c] = T(fmaf(m.dt[r], du, D * dv));
+        if (r < n) dx[((row0 + r) * in.H + h) * P + c] = fmaf(m.dt[r], du, D * dv);
       }
       xdu = half_sum(xdu);
       qq = half_sum(qq);
@@ -682,7 +683,7 @@ chunk_grad_kernel(const In<T> in, const T *__restrict__ dy, const float *__restr
       const int r = tid + 32 * k;
       if (r < n) {
         const float d = fmaf(A, m.l[r], m.xdu[r]) * m.sig[r];
-        draw[(row0 + r) * in.H + h] = T(d);
+        draw[(row0 + r) * in.H + h] = d;
         dA = fmaf(m.dt[r], m.l[r], dA);
         db += d;
       }
