@@ -306,10 +306,13 @@ boundaries_kernel(const In<float> in, const float *__restrict__ dy, const float 
 // state's HBM traffic, N x 64 fp32 read and written once; B and C are read
 // by every head of a group and stay in the caches.  The decay is two floats:
 // nothing but the state goes from token to token, so that the rounding of one
-// float, token after token, would add up (8e-6 in 600 tokens of steps 1e-4 at
-// A = -0.1).
+// float, token after token, would add up (2.8e-5 in 600 tokens of steps 1e-4 at
+// A = -0.1).  The step is loaded in front of the state, so that its arithmetic
+// is done when the state arrives, and the CTAs an SM are held to what hides the
+// rest: 256 x 32 states of 128 x 128 165 us with four (bf16, whose bytes take 164
+// at the copy rate; fp32 181), 210 with three.
 template <typename T, int N>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, N == 128 ? 4 : 6)
 decode_kernel(const In<T> in, float *state, T *__restrict__ y) {
   __shared__ __align__(16) float4 part[16][16];
   const int tid = threadIdx.x, c4 = tid & 15, r = tid >> 4;  // columns 4 c4 .., rows r, r + 16, ..
@@ -318,13 +321,15 @@ decode_kernel(const In<T> in, float *state, T *__restrict__ y) {
   const long long s = blockIdx.x / npt / in.H;
   const int g = h / (in.H / in.G);
   float *st = state + (s * in.H + h) * (long long)N * in.P + pt * 64 + c4 * 4;
+  const T raw = in.raw[s * in.rs + h];
+  const float A = in.A[h], bias = in.bias ? in.bias[h] : 0.0f;
   float4 v[N / 16];
 #pragma unroll
   for (int i = 0; i < N / 16; ++i)
     v[i] = *reinterpret_cast<const float4 *>(st + (long long)(r + 16 * i) * in.P);
-  const float dt = softplus(to_f32(in.raw[s * in.rs + h]) + (in.bias ? in.bias[h] : 0.0f));
+  const float dt = softplus(to_f32(raw) + bias);
   float a, al;
-  exp_pair(dt * in.A[h], a, al);
+  exp_pair(dt * A, a, al);
   const float4 x = load4(in.x + s * in.xs + (long long)h * in.P + pt * 64 + c4 * 4);
   const T *bp = in.B + s * in.bs + g * N, *cp = in.C + s * in.cs + g * N;
   const uint64_t a2 = f2_pack(a, a), al2 = f2_pack(al, al), x01 = f2_pack(x.x, x.y), x23 = f2_pack(x.z, x.w);
