@@ -5,9 +5,10 @@
  * status codes as gdn_qdq.h: every pointer is caller-owned device memory,
  * nothing is allocated, argument errors are returned before any launch, calls
  * are asynchronous on `cuda_stream`, a malformed cu_seqlens skips the
- * sequences concerned (their outputs are left as they were; what the other
- * sequences of that call receive is not defined) and is reported by
- * gdn_last_error().  All sums, states and statistics are fp32; a result is
+ * sequences concerned (those that are no range of the call's tokens, and those
+ * that start before the one in front of them; their outputs are left as they
+ * were; what the other sequences of that call receive is not defined) and is
+ * reported by gdn_last_error().  All sums, states and statistics are fp32; a result is
  * rounded once, to its own type.  Results do not depend on timing: nothing is
  * added in an order that changes from run to run.
  *
@@ -83,7 +84,9 @@ gdn_status gdn_conv_backward(const void *x, int64_t x_stride, const float *weigh
  * zeros, state_out may alias state_in exactly; an empty sequence passes its
  * state through.
  * bf16 calls work on 64-token chunks: a NaN or an infinity in x, B or C can
- * reach the outputs of the tokens before it in its chunk, and those behind it.
+ * reach the outputs of the tokens before it in its chunk, and those behind it;
+ * gradients of either type work on such chunks too.  An infinity in a state
+ * stays one until a decay of zero.
  * P, N in {64, 128}; H a multiple of G.  x, B, C, y and the states 16-byte
  * aligned, the strides of x, B and C multiples of 16 bytes; dt_raw
  * element-aligned with any stride.
@@ -114,6 +117,9 @@ gdn_status gdn_scan_decode(const void *x, int64_t x_stride, const void *dt_raw,
  * contiguous) and dstate_out (fp32, or NULL for zero).  Contiguous outputs in
  * dtype dtype: dx, ddt (of dt_raw), dB, dC (summed over the heads of a group);
  * fp32: dA [H], dD [H], ddt_bias [H], dstate_in [n_seq, H, N, P].
+ * The workspace holds a state and its adjoint for every 64 tokens, 12 bytes an
+ * element in bf16 calls and 8 in fp32 ones (4 GB for 8 x 4096 tokens of 80 heads
+ * of 128 x 64 in bf16).
  */
 size_t gdn_scan_backward_workspace_bytes(int n_seq, int T, int H, int P, int G, int N,
                                          gdn_dtype dtype, int packed);
@@ -145,7 +151,7 @@ gdn_status gdn_scan_backward(const void *x, int64_t x_stride, const void *dt_raw
  * scale 0 and codes 0; a row or group that holds a NaN has a NaN scale.
  * The mean is fp32: a row of which mean(s^2) + eps is 0 there (eps = 0 and
  * values below 1e-22 at most) has y = 0 and gradients of zero but for
- * dresidual; one whose squares pass 3e38 has y = 0.
+ * dresidual; one whose sum of squares passes 3e38 has y = 0.
  * d: up to 4096 vectors of 16 bytes, or 8192 elements where pointers, strides
  * or d do not allow vectors; the INT8 groups need them (and d a multiple of
  * the group).

@@ -103,10 +103,12 @@ struct Tile {
 };
 
 // Whether sequence s of cu is a range inside the T packed tokens that the
-// first sequence starts and the last one ends.
+// first sequence starts and the last one ends, and that does not step back
+// behind the start of the one in front of it, whose tokens it would write over.
 __device__ __forceinline__ bool seq_ok(const int *__restrict__ cu, int n_seq, int s, int T) {
   const int a = cu[s], b = cu[s + 1];
-  return a >= 0 && b >= a && b <= T && (s != 0 || a == 0) && (s != n_seq - 1 || b == T);
+  return a >= (s != 0 ? max(cu[s - 1], 0) : 0) && b >= a && b <= T && (s != 0 || a == 0) &&
+         (s != n_seq - 1 || b == T);
 }
 
 // The tile of `slot`, found by a whole warp: each round probes 32 sequences
