@@ -439,7 +439,12 @@ constexpr int kMaxCtas = 148 * 4;
 // four vectors each in flight (16384 x 2048 bf16 with a residual to E4M3: 44
 // us, 81 % of the copy rate, with 64 threads of four; 47 with a warp of
 // eight, 48 with 128 of two, 53 with 256 of one).  The gradient, which holds three to four
-// tensors of two rows, keeps to two vectors a thread where it can.
+// tensors of two rows, keeps to two vectors a thread where it can.  CTAs of 512
+// threads and more leave it too few registers for them: bf16 rows above 4096
+// with a gate spill 216 to 280 bytes, all above 8192 256 to 892, above 16384, with
+// four vectors, 0.9 to 2.3 KB.  33.5 million elements, bf16, with a residual's
+// gradient and a gate: 101 us at d = 4096, 114 at 8192, 373 at 16384 (the bytes
+// take 61); without a gate 54 at 2048, 146 at 16384 (41).
 #define GDN_NORM_SHAPE(nv, CALL)          \
   ((nv) <= 8      ? CALL(8, 1)            \
    : (nv) <= 16   ? CALL(16, 1)           \
