@@ -7,8 +7,9 @@
 // 1.4e-4 (2-norm) where a 32-bit form differs by 2.5e-5; now by 2.5e-5 to
 // 4.6e-5, in no more time (383 us the call).  A third piece of M would take dx
 // from 7.7e-5 to 3.9e-5 for 10 us.  What dA and ddt_bias add up over all tokens
-// is kept to fp32's own rounding: Z stays fp32, x_t . du_t is taken from Z's
-// columns instead of du, and the states and adjoints come in three pieces
+// is kept to fp32's own rounding: Z stays fp32 and its factors are summed outside
+// the tensor pipe, x_t . du_t is taken from Z's columns instead of du, and the
+// states and adjoints come in three pieces
 // (with two, dA was up to 8e-6 off; the third costs 45 us of the 222 below).
 //
 // A CTA of sixteen warps takes one chunk and a range of one group's heads.
@@ -57,6 +58,16 @@ struct GradSmem {
 __device__ __forceinline__ float quad_sum(float v) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// d += a b with the products of one step in the tensor pipe and the sum in fp32:
+// the pipe truncates a sum (towards zero, 2^-24 of it on average), and what Z
+// is made of would lose that eight times over.
+__device__ __forceinline__ void add_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+  mma16816(t, a, b0, b1);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d[e] += t[e];
 }
 
 // dst: bf16 [tokens, G, N], or with parts fp32 [tokens, G, splits, N].
@@ -155,8 +166,8 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
         uint32_t a[4], b[4];
         ldsm4(block_rows<N>(sC, sr, 2 * kk, lane), a);
         ldsm4(block_cols<N>(sB, sc, 2 * kk, lane), b);
-        mma16816(S[0], a, b[0], b[1]);
-        mma16816(S[1], a, b[2], b[3]);
+        add_mma(S[0], a, b[0], b[1]);
+        add_mma(S[1], a, b[2], b[3]);
       }
     }
     // K = dy x^T, then M, W and Z
@@ -173,8 +184,8 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
         uint32_t a[4], b[4];
         ldsm4(block_rows<64>(ty, sr, 2 * (kk % 4), lane), a);
         ldsm4(block_cols<64>(tx, sc, 2 * (kk % 4), lane), b);
-        mma16816(K[0], a, b[0], b[1]);
-        mma16816(K[1], a, b[2], b[3]);
+        add_mma(K[0], a, b[0], b[1]);
+        add_mma(K[1], a, b[2], b[3]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -272,7 +283,8 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
     }
     float rsum[2] = {0.f, 0.f}, qsum[2] = {0.f, 0.f};
     const float Dh = in.D ? in.D[h] : 0.0f;
-    // T = dy H0 (side 0) or x G (side 1) from `pieces` tiles at tS; its
+    // T = dy H0 (side 0) or x G (side 1) from `pieces` tiles at tS, the small
+    // ones first, whose sums the pipe truncates at their own magnitude; its
     // scaled rows join dC or dB, their products with C or B the row sums
     auto with_state = [&](int side, uint32_t tA, uint32_t tS, int pieces) {
       const uint32_t tO = side ? sB : sC;
@@ -282,12 +294,12 @@ chunk_grad_mma_kernel(const In<__nv_bfloat16> in, const __nv_bfloat16 *__restric
 #pragma unroll
         for (int e = 0; e < 4; ++e) T[j][e] = 0.0f;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t a[4];
-        ldsm4(block_rows<64>(tA, gr, 2 * kk, lane), a);
+      for (int piece = 1; piece >= 0; --piece) {
+        if (piece >= pieces) continue;
 #pragma unroll
-        for (int piece = 0; piece < 2; ++piece) {
-          if (piece >= pieces) break;
+        for (int kk = 0; kk < 4; ++kk) {
+          uint32_t a[4];
+          ldsm4(block_rows<64>(tA, gr, 2 * kk, lane), a);
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             uint32_t b[4];
