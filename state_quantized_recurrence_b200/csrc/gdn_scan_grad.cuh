@@ -5,24 +5,24 @@
 // in fp32: with pairs, and the tensor pipe's truncating sums running on over
 // 16 heads, the two differed from the rounded 64-bit gradient by 1.0e-4 to
 // 1.4e-4 (2-norm) where a 32-bit form differs by 2.5e-5; now by 2.5e-5 to
-// 4.6e-5, in no more time (383 us the call).  A third piece of M would take dx
+// 4.6e-5, in no more time (386 us the call).  A third piece of M would take dx
 // from 7.7e-5 to 3.9e-5 for 10 us.  What dA and ddt_bias add up over all tokens
-// is kept to fp32's own rounding: Z stays fp32 and its factors are summed outside
-// the tensor pipe, x_t . du_t is taken from Z's columns instead of du, and the
-// states and adjoints come in three pieces
-// (with two, dA was up to 8e-6 off; the third costs 45 us of the 222 below).
+// is kept to fp32's own rounding: Z stays fp32 and its factors are summed
+// outside the tensor pipe, x_t . du_t is taken from Z's columns instead of du,
+// and the states and adjoints come in three pieces (with two, dA was up to
+// 8e-6 off; the third costs 45 us of the 229 below).
 //
 // A CTA of sixteen warps takes one chunk and a range of one group's heads.
 // S = C B^T is formed once; dB and dC are summed over the heads in registers,
 // so that neither leaves the SM before it is whole (with the heads split over
 // several CTAs, their fp32 parts are added afterwards in order).
 //
-// 2 x 4096 tokens x 16 heads, N = 128, P = 64: 222 us, 26 thousand cycles a
+// 2 x 4096 tokens x 16 heads, N = 128, P = 64: 229 us, 27 thousand cycles a
 // head and chunk for 6.6 of tensor pipe and 12.5 of shared-memory pipe (25 and
 // 48 % busy); the rest is the latency of dependent stages between seven
 // barriers.  Eight warps with twice the tile ran the same with states in two
-// pieces (181 us against 188).  N = 128 spills 32 (P = 64) and 80 bytes (P = 128)
-// of the sixteen warps' 128 registers, addresses and a head's scalars.
+// pieces (181 us against 188).  The 128 registers that sixteen warps leave spill
+// 24 to 104 bytes, addresses and a head's scalars.
 #pragma once
 
 #include "gdn_scan_mma.cuh"
