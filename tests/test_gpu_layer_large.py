@@ -104,3 +104,54 @@ def test_norm_of_many_rows(cuda_lib, rows, d, dtype):
     want, kept = ref.norm(x, w, res, z, dtype=dtype)
     ref.within(y, want, want.abs(), d // 8 + 74, "y")
     assert torch.equal(s.double().cpu(), kept)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,T", [(3000, 3), (300, 70), (257, 1)])
+def test_many_packed_sequences(cuda_lib, n, T, dtype):
+    """More packed sequences than are ranked by length or found in one probe:
+    the bits of the dense call over the same sequences."""
+    g = torch.Generator().manual_seed(11)
+    r = lambda *s: torch.randn(*s, generator=g).to(dtype).cuda()
+    H, P, G, N, C = 2, 64, 1, 64, 24
+    x, raw, B, Cm, dy = r(n, T, H, P), r(n, T, H), r(n, T, G, N), r(n, T, G, N), r(n, T, H, P)
+    A, D = -torch.rand(H, generator=g).cuda() - 0.5, torch.randn(H, generator=g).cuda()
+    st = torch.randn(n, H, N, P, generator=g).cuda()
+    u, w, b, cs, du = r(n, T, C), torch.randn(C, 4, generator=g).cuda(), \
+        torch.randn(C, generator=g).cuda(), r(n, 3, C), r(n, T, C)
+    cu = (torch.arange(n + 1, dtype=torch.int32) * T).cuda()
+    one = lambda t: t.reshape(1, n * T, *t.shape[2:])
+
+    def scan(f, cu):
+        a = (f(x), f(raw), A, f(B), f(Cm))
+        kw = dict(D=D, state_in=st, cu_seqlens=cu)
+        return cuda_lib.gdn_scan_prefill(*a, **kw) + tuple(
+            cuda_lib.gdn_scan_backward(*a, f(dy), dstate_out=st, **kw)[i] for i in (0, 1, 3, 4, 7))
+
+    def conv(f, cu):
+        back = cuda_lib.gdn_conv_backward(f(u), w, f(du), b, cs, cu, cs)
+        return cuda_lib.gdn_conv_prefill(f(u), w, b, cs, cu) + (back[0], back[3])
+
+    for op in (scan, conv):
+        for i, (p, q) in enumerate(zip(op(lambda t: t, None), op(one, cu))):
+            assert torch.equal(p.reshape(-1), q.reshape(-1)), (op.__name__, i)
+    cuda_lib.check_last_error()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_tokens(cuda_lib, dtype):
+    """Dense calls of no tokens pass their states and gradients through."""
+    n, H, P, N, C = 3, 2, 64, 64, 8
+    e = lambda *s: torch.empty(n, 0, *s, dtype=dtype, device="cuda")
+    st = torch.randn(n, H, N, P, device="cuda")
+    A = -torch.ones(H, device="cuda")
+    scan = (e(H, P), e(H), A, e(1, N), e(1, N))
+    y, last = cuda_lib.gdn_scan_prefill(*scan, state_in=st)
+    assert y.shape == (n, 0, H, P) and torch.equal(last, st)
+    got = cuda_lib.gdn_scan_backward(*scan, e(H, P), state_in=st, dstate_out=st)
+    assert torch.equal(got[7], st) and all((got[i] == 0).all() for i in (2, 5, 6))
+    w, cs = torch.randn(C, 4, device="cuda"), torch.randn(n, 3, C, device="cuda").to(dtype)
+    y, last = cuda_lib.gdn_conv_prefill(e(C), w, None, cs)
+    assert y.shape == (n, 0, C) and torch.equal(last, cs)
+    got = cuda_lib.gdn_conv_backward(e(C), w, e(C), None, cs, None, cs)
+    assert torch.equal(got[3], cs) and (got[1] == 0).all() and (got[2] == 0).all()

@@ -221,3 +221,25 @@ def test_sums_of_products_are_not_truncated(cuda_lib, n, T):
     got = backward(cuda_lib, t)
     want = long.scan_grad(*args(t), t["dy"], t["dlast"])[2:]
     assert long.off(got[5], want[5]) <= 1.5 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,T,H,step,A", [(1, 8192, 2, 1e-4, 0.1), (2, 2048, 32, 1e-3, 1.0)])
+def test_gradients_of_slowly_forgetting_states(cuda_lib, n, T, H, step, A, dtype):
+    """The adjoint runs back over thousands of tokens as the state runs forward:
+    the bounds of test_states_of_long_prompts (bf16) and
+    test_a_state_that_forgets_almost_nothing (fp32), and for dB and dC those of
+    test_gradients_summed_over_many_heads, where a state or an adjoint enters
+    with its own bound."""
+    t = make(9, (n, T), n, H, 64, 1, 64, dtype, step, (A, A))
+    got = backward(cuda_lib, t)
+    want = long.scan_grad(*args(t), t["dy"], t["dlast"])[2:]
+    if dtype == BF16:
+        state = (12 * 2.0 + 1) * 2.0 ** -24 + math.sqrt(T / 64) * 2.0 ** -24 + 2.0 ** -21
+        sums = rounding(2.0 ** -20 + state)
+    else:
+        state = math.sqrt(T) * 2.0 ** -25 + 2.0 ** -21
+        sums = 2 * state
+    for i, name, bound in ((7, "dstate_in", state), (5, "dD", state), (3, "dB", sums),
+                           (4, "dC", sums)):
+        assert long.off(got[i], want[i].to(got[i].dtype)) <= bound, name
